@@ -416,6 +416,77 @@ int moe_layer_bwd(const moe_config* cfg, const void* dY, float d_aux, const void
                   const void* W_g, const void* W_u, const void* W_d, const void* saved, void* dX, void* dW_r,
                   void* dW_g, void* dW_u, void* dW_d, float* dlogits, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * RMSNorm of the residual stream, with the residual's addition: the norm that
+ * makes the layer's (and moe_ffn_fwd's) x. Per row t of H:
+ *   h = x + residual (residual NULL: h = x), rstd = 1 / sqrt(mean(h^2) + eps),
+ *   y = h * rstd * weight,
+ * all in fp32 from the unrounded h, each output rounded once. Outputs, each
+ * optional (NULL to skip; at least one of h, y, y_q): h [T,H] bf16; y [T,H]
+ * bf16; y_q e4m3 [T,H] with y_sf ue8m0 [T,H/32], the MXFP8 quantisation of the
+ * fp32 y (1x32 blocks along H, the rule of moe_quantize_mxfp8; both or
+ * neither); rstd [T] fp32, for the backward.
+ *   x, residual [T,H] bf16, weight [H] bf16. h may be x or residual itself, y
+ *   may be x itself; other overlaps of outputs with inputs are not allowed.
+ *   T >= 1, H % 8 == 0 (H % 32 == 0 with y_q), H <= 16384, eps >= 0.
+ *
+ * moe_rmsnorm_bwd: the derivative for upstream dY of y and dh of h (dh NULL:
+ * h has no other use), with xhat = h rstd and g = weight dY:
+ *   dX = dh + rstd (g - xhat mean(g xhat))  (the gradient of x and of residual),
+ *   dweight = sum_t dY xhat (fp32 [H], summed in a fixed order).
+ *   dY, h, dh, dX [T,H] bf16; rstd as the forward wrote it. dX or dweight may
+ *   be NULL (not both). dX may be dY, h or dh itself. ws is needed when
+ *   dweight is not NULL.
+ * ------------------------------------------------------------------------ */
+int moe_rmsnorm_fwd(int32_t T, int32_t H, const void* x, const void* residual, const void* weight, float eps, void* h,
+                    void* y, uint8_t* y_q, uint8_t* y_sf, float* rstd, void* stream);
+size_t moe_rmsnorm_bwd_workspace_size(int32_t T, int32_t H);
+int moe_rmsnorm_bwd(int32_t T, int32_t H, const void* dY, const void* h, const void* weight, const float* rstd,
+                    const void* dh, void* dX, float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gated feed-forward block on its own: y = W_d (silu(W_g x) * (W_u x)) -- a
+ * dense layer of the stack, or a shared expert outside moe_layer_fwd (whose
+ * backward has none). From one token (the weights are streamed once) to whole
+ * batches.
+ *   BF16: x [T,H], W_g, W_u [F,H], W_d [H,F] bf16, *_sf NULL; the activation
+ *     silu(g) u is rounded to bf16 between the products (fp32 accumulate). H,
+ *     F multiples of 8.
+ *   MXFP8: the weights as e4m3 with ue8m0 scales (moe_quantize_mxfp8); x bf16
+ *     with x_sf NULL (quantised on the way), or e4m3 codes with x_sf [T,H/32]
+ *     (as moe_rmsnorm_fwd writes them); the activation is quantised from its
+ *     fp32 value. H % 256 == 0, F % 128 == 0, save_for_bwd = 0. Scale pointers
+ *     4-byte aligned.
+ *   NVFP4: MOE_ERR_UNSUPPORTED.
+ *   y [T,H] bf16, not overlapping the inputs. saved: moe_ffn_saved_size()
+ *   bytes when save_for_bwd (else NULL): the bf16 gate and up pre-activations
+ *   and the activation.
+ *   T <= 2^24; H, F <= 2^20.
+ *
+ * moe_ffn_bwd: the derivative for upstream dY [T,H] bf16 (BF16, save_for_bwd
+ * = 1), fp32 accumulate, with v = W_d^T dY and s = sigmoid(g):
+ *   dgate = v u s (1 + g (1 - s)), dup = v g s (rounded to bf16),
+ *   dX = W_g^T dgate + W_u^T dup, dW_g = sum_t dgate x^T, dW_u = sum_t dup x^T,
+ *   dW_d = sum_t dY a^T, all bf16, overwritten. dX, the pair dW_g and dW_u, and
+ *   dW_d may each be NULL (not all), so that data and weight gradients can be
+ *   run apart; x is read for dW_g/dW_u and W_g, W_u for dX only (else NULL).
+ *   Outputs must not overlap the inputs or each other.
+ * ------------------------------------------------------------------------ */
+typedef struct moe_ffn_config {
+    int32_t T, H, F;
+    int32_t dtype;        /* moe_dtype of the operands: BF16 or MXFP8 */
+    int32_t save_for_bwd; /* 1: moe_ffn_fwd fills `saved` for moe_ffn_bwd */
+} moe_ffn_config;
+size_t moe_ffn_workspace_size(const moe_ffn_config* cfg);
+size_t moe_ffn_saved_size(const moe_ffn_config* cfg);
+int moe_ffn_fwd(const moe_ffn_config* cfg, const void* x, const uint8_t* x_sf, const void* W_g, const void* W_u,
+                const void* W_d, const uint8_t* W_g_sf, const uint8_t* W_u_sf, const uint8_t* W_d_sf, void* y,
+                void* saved, void* ws, size_t ws_bytes, void* stream);
+size_t moe_ffn_bwd_workspace_size(const moe_ffn_config* cfg);
+int moe_ffn_bwd(const moe_ffn_config* cfg, const void* dY, const void* x, const void* W_g, const void* W_u,
+                const void* W_d, const void* saved, void* dX, void* dW_g, void* dW_u, void* dW_d, void* ws,
+                size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -39,10 +39,17 @@ class moe_config(ctypes.Structure):
                 ("capacity_factor", ctypes.c_float), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32)]
 
 
+class moe_ffn_config(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("F", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("save_for_bwd", ctypes.c_int32)]
+
+
 _VP = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
 _CFG = ctypes.POINTER(moe_config)
+_FFN = ctypes.POINTER(moe_ffn_config)
+_I32 = ctypes.c_int32
 
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -80,6 +87,14 @@ _SIGS = {
     "moe_layer_bwd_mxfp8_workspace_size": (_SZ, [_CFG]),
     "moe_layer_bwd_mxfp8": (_I, [_CFG, _VP, ctypes.c_float, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                  _VP, _VP, _VP, _SZ, _VP]),
+    "moe_rmsnorm_fwd": (_I, [_I32, _I32, _VP, _VP, _VP, ctypes.c_float, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "moe_rmsnorm_bwd_workspace_size": (_SZ, [_I32, _I32]),
+    "moe_rmsnorm_bwd": (_I, [_I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "moe_ffn_workspace_size": (_SZ, [_FFN]),
+    "moe_ffn_saved_size": (_SZ, [_FFN]),
+    "moe_ffn_fwd": (_I, [_FFN, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "moe_ffn_bwd_workspace_size": (_SZ, [_FFN]),
+    "moe_ffn_bwd": (_I, [_FFN, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
 }
 
 
@@ -326,3 +341,51 @@ def moe_layer_bwd_mxfp8(cfg, dY, d_aux, x, W_r, W_dT, W_dT_sf, W_guT, W_guT_sf, 
         ctypes.byref(cfg), _p(dY), ctypes.c_float(d_aux), _p(x), _p(W_r), _p(W_dT), _p(W_dT_sf), _p(W_guT),
         _p(W_guT_sf), _p(saved), _p(dX), _p(dW_r), _p(dW_g), _p(dW_u), _p(dW_d), _p(dlogits), _p(ws),
         ws.numel() if ws is not None else 0, _st(stream)))
+
+
+def moe_rmsnorm_fwd(x, residual, weight, eps, h, y, y_q, y_sf, rstd, stream=None):
+    """x, residual [..., H] bf16 (residual or None); outputs h, y, y_q + y_sf, rstd may each be None."""
+    H = x.shape[-1]
+    return _check("moe_rmsnorm_fwd", load().moe_rmsnorm_fwd(
+        x.numel() // H, H, _p(x), _p(residual), _p(weight), eps, _p(h), _p(y), _p(y_q), _p(y_sf), _p(rstd),
+        _st(stream)))
+
+
+def moe_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
+    return load().moe_rmsnorm_bwd_workspace_size(T, H)
+
+
+def moe_rmsnorm_bwd(dY, h, weight, rstd, dh, dX, dweight, ws, stream=None):
+    H = h.shape[-1]
+    return _check("moe_rmsnorm_bwd", load().moe_rmsnorm_bwd(
+        h.numel() // H, H, _p(dY), _p(h), _p(weight), _p(rstd), _p(dh), _p(dX), _p(dweight), _p(ws),
+        ws.numel() if ws is not None else 0, _st(stream)))
+
+
+def make_ffn_config(T, H, F, dtype="bf16", save_for_bwd=0) -> moe_ffn_config:
+    return moe_ffn_config(T=T, H=H, F=F, dtype=_DTYPES[dtype] if isinstance(dtype, str) else dtype,
+                          save_for_bwd=save_for_bwd)
+
+
+def moe_ffn_workspace_size(cfg) -> int:
+    return load().moe_ffn_workspace_size(ctypes.byref(cfg))
+
+
+def moe_ffn_saved_size(cfg) -> int:
+    return load().moe_ffn_saved_size(ctypes.byref(cfg))
+
+
+def moe_ffn_fwd(cfg, x, x_sf, W_g, W_u, W_d, W_g_sf, W_u_sf, W_d_sf, y, saved, ws, stream=None):
+    return _check("moe_ffn_fwd", load().moe_ffn_fwd(
+        ctypes.byref(cfg), _p(x), _p(x_sf), _p(W_g), _p(W_u), _p(W_d), _p(W_g_sf), _p(W_u_sf), _p(W_d_sf), _p(y),
+        _p(saved), _p(ws), ws.numel() if ws is not None else 0, _st(stream)))
+
+
+def moe_ffn_bwd_workspace_size(cfg) -> int:
+    return load().moe_ffn_bwd_workspace_size(ctypes.byref(cfg))
+
+
+def moe_ffn_bwd(cfg, dY, x, W_g, W_u, W_d, saved, dX, dW_g, dW_u, dW_d, ws, stream=None):
+    return _check("moe_ffn_bwd", load().moe_ffn_bwd(
+        ctypes.byref(cfg), _p(dY), _p(x), _p(W_g), _p(W_u), _p(W_d), _p(saved), _p(dX), _p(dW_g), _p(dW_u), _p(dW_d),
+        _p(ws), ws.numel() if ws is not None else 0, _st(stream)))

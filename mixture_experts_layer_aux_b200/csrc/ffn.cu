@@ -1,0 +1,294 @@
+// ffn.cu -- the gated feed-forward block y = W_d (silu(W_g x) * (W_u x)) on its
+// own (a dense layer of the stack, or a shared expert), forward in bf16 and
+// MXFP8 and backward in bf16.
+//   few tokens    the streaming kernels of skinny.cuh (two launches; MXFP8 from
+//                 a bf16 x: three);
+//   more, bf16    the dense tensor-core kernel of dense.cuh;
+//   more, MXFP8   the block-scaled grouped GEMM as one group.
+// Backward: dgrad of the down projection with the SwiGLU backward in its
+// epilogue, the weight gradients, and dX = dgate W_g + dup W_u as one product
+// over [dgate | dup].
+#include "common.cuh"
+#include "dense.cuh"
+#include "layout.h"
+#include "skinny.cuh"
+
+namespace moe_impl {
+int gemm_gateup_mx(int rows, int groups, int H, int F, const void* A, const uint8_t* A_sf, const void* Wg,
+                   const uint8_t* Wg_sf, const void* Wu, const uint8_t* Wu_sf, const int32_t* offsets,
+                   const float* row_gate, void* C, uint8_t* C_sf, void* save, cudaStream_t st);
+int gemm_down_mx(int rows, int groups, int H, int F, const void* A, const uint8_t* A_sf, const void* Wd,
+                 const uint8_t* Wd_sf, const int32_t* offsets, void* C, cudaStream_t st);
+}  // namespace moe_impl
+
+namespace ffn {
+
+using dense::Params;
+
+// Tokens up to which the streaming kernels are taken.
+constexpr int SKINNY_T = skinny::MAX_T;
+
+#define FFN_RC(x)         \
+  do {                    \
+    int _rc = (x);        \
+    if (_rc) return _rc;  \
+  } while (0)
+
+static bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+static bool a4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static int check_cfg(const moe_ffn_config* c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->T < 1 || c->H < 1 || c->F < 1) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_DT_BF16 && c->dtype != MOE_DT_MXFP8 && c->dtype != MOE_DT_NVFP4) return MOE_ERR_INVALID_ARG;
+  if (c->dtype == MOE_DT_NVFP4) return MOE_ERR_UNSUPPORTED;
+  if (c->T > (1 << 24) || c->H > (1 << 20) || c->F > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  if (c->dtype == MOE_DT_MXFP8) {
+    if (c->H % 256 != 0 || c->F % 128 != 0 || c->save_for_bwd) return MOE_ERR_UNSUPPORTED;
+  } else if (c->H % 8 != 0 || c->F % 8 != 0) {
+    return MOE_ERR_UNSUPPORTED;
+  }
+  return MOE_OK;
+}
+
+struct FwdWs {
+  __nv_bfloat16* a;
+  float* part;
+  uint8_t *xq, *xq_sf, *aq, *aq_sf;
+  int32_t* off;
+};
+static size_t carve_fwd(void* ws, const moe_ffn_config* c, FwdWs* w) {
+  Carve cv(ws);
+  const size_t T = c->T, H = c->H, F = c->F;
+  *w = FwdWs{};
+  if (c->dtype == MOE_DT_MXFP8) {
+    w->xq = cv.take<uint8_t>(T * H);
+    w->xq_sf = cv.take<uint8_t>(T * H / 32);
+    w->aq = cv.take<uint8_t>(T * F);
+    w->aq_sf = cv.take<uint8_t>(T * F / 32);
+    w->off = cv.take<int32_t>(2);
+  } else {
+    if (!c->save_for_bwd) w->a = cv.take<__nv_bfloat16>(T * F);
+    if (c->T > SKINNY_T) w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
+  }
+  return cv.used;
+}
+
+struct Saved {
+  __nv_bfloat16* gateup;  // [T, 2F]: gate in columns [0, F), up in [F, 2F)
+  __nv_bfloat16* a;       // [T, F]
+};
+static size_t carve_saved(void* p, const moe_ffn_config* c, Saved* s) {
+  Carve cv(p);
+  s->gateup = cv.take<__nv_bfloat16>((size_t)c->T * 2 * c->F);
+  s->a = cv.take<__nv_bfloat16>((size_t)c->T * c->F);
+  return cv.used;
+}
+
+struct BwdWs {
+  __nv_bfloat16* dgu;  // [T, 2F]: dgate | dup
+  float* part;
+};
+static size_t carve_bwd(void* ws, const moe_ffn_config* c, BwdWs* w) {
+  Carve cv(ws);
+  w->dgu = cv.take<__nv_bfloat16>((size_t)c->T * 2 * c->F);
+  w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
+  return cv.used;
+}
+
+// bf16 [outer, inner] with a row stride of ld elements, boxes of 64 x box_outer.
+static bool tmap(CUtensorMap* m, const void* base, long long inner, long long outer, long long ld, int box_outer) {
+  return moe_host::encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, (uint64_t)ld * 2, 64,
+                                  box_outer);
+}
+static int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+static Params base_params(int M, int N, int KB, float* part, void* C, long long ldc) {
+  Params p{};
+  p.M = M;
+  p.N = N;
+  p.KB = KB;
+  p.tiles_m = p.tm_split = cdiv(M, dense::BM);
+  p.part = part;
+  p.C = static_cast<__nv_bfloat16*>(C);
+  p.ldc = ldc;
+  p.status = moe_host::device_status_ptr();
+  return p;
+}
+
+static int gateup(int T, int H, int F, const void* x, const void* Wg, const void* Wu, void* a, void* save, float* part,
+                  cudaStream_t st, bool dep) {
+  Params p = base_params(T, F, cdiv(H, dense::BK), part, a, F);
+  if (!tmap(&p.tmA, x, H, T, H, 128) || !tmap(&p.tmB0, Wg, H, F, H, 128) || !tmap(&p.tmB1, Wu, H, F, H, 128))
+    return MOE_ERR_CUDA;
+  p.save = static_cast<__nv_bfloat16*>(save);
+  return dense::launch<dense::OP_GATEUP>(p, st, dep);
+}
+
+static int down(int T, int H, int F, const void* a, const void* Wd, void* y, float* part, cudaStream_t st, bool dep) {
+  Params p = base_params(T, H, cdiv(F, dense::BK), part, y, H);
+  if (!tmap(&p.tmA, a, F, T, F, 128) || !tmap(&p.tmB0, Wd, F, H, F, 128)) return MOE_ERR_CUDA;
+  return dense::launch<dense::OP_DOWN>(p, st, dep);
+}
+
+static int dgrad_act(int T, int H, int F, const void* dY, const void* Wd, const void* gateup, void* dgu, float* part,
+                     cudaStream_t st, bool dep) {
+  Params p = base_params(T, F, cdiv(H, dense::BK), part, dgu, 2LL * F);
+  if (!tmap(&p.tmA, dY, H, T, H, 128) || !tmap(&p.tmB0, Wd, F, H, F, 64)) return MOE_ERR_CUDA;
+  p.gateup = static_cast<const __nv_bfloat16*>(gateup);
+  return dense::launch<dense::OP_DGRAD_ACT>(p, st, dep);
+}
+
+static int dgrad_x(int T, int H, int F, const __nv_bfloat16* dgu, const void* Wg, const void* Wu, void* dX,
+                   float* part, cudaStream_t st, bool dep) {
+  const int kb = cdiv(F, dense::BK);
+  Params p = base_params(T, H, 2 * kb, part, dX, H);
+  p.kb_split = kb;
+  if (!tmap(&p.tmA, dgu, F, T, 2LL * F, 128) || !tmap(&p.tmA2, dgu + F, F, T, 2LL * F, 128) ||
+      !tmap(&p.tmB0, Wg, H, F, H, 64) || !tmap(&p.tmB1, Wu, H, F, H, 64))
+    return MOE_ERR_CUDA;
+  return dense::launch<dense::OP_DGRAD_X>(p, st, dep);
+}
+
+// dW [M, N] = sum_t dO[t, :M]^T act[t, :N]; with dO2, a second [M, N] from it into dW2 in the same launch.
+static int wgrad(int T, int M, int N, const void* dO, const void* dO2, long long ld_dO, const void* act, void* dW,
+                 void* dW2, float* part, cudaStream_t st, bool dep) {
+  Params p = base_params(M, N, cdiv(T, dense::BK), part, dW, N);
+  if (!tmap(&p.tmA, dO, M, T, ld_dO, 64) || !tmap(&p.tmB0, act, N, T, N, 64)) return MOE_ERR_CUDA;
+  if (dO2) {
+    if (!tmap(&p.tmA2, dO2, M, T, ld_dO, 64)) return MOE_ERR_CUDA;
+    p.tiles_m = 2 * p.tm_split;
+    p.C2 = static_cast<__nv_bfloat16*>(dW2);
+  }
+  return dense::launch<dense::OP_WGRAD>(p, st, dep);
+}
+
+static skinny::Params skinny_params(int T, int N, int K, const void* W0, const void* W1, const uint8_t* sf0,
+                                    const uint8_t* sf1, const void* x, const uint8_t* x_sf, void* out,
+                                    uint8_t* out_sf, void* save) {
+  skinny::Params p{};
+  p.W0 = static_cast<const uint8_t*>(W0);
+  p.W1 = static_cast<const uint8_t*>(W1);
+  p.sf0 = sf0;
+  p.sf1 = sf1;
+  p.x = static_cast<const uint8_t*>(x);
+  p.x_sf = x_sf;
+  p.out = out;
+  p.out_sf = out_sf;
+  p.save = static_cast<__nv_bfloat16*>(save);
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  return p;
+}
+
+static int fwd_bf16(const moe_ffn_config* c, const void* x, const void* Wg, const void* Wu, const void* Wd, void* y,
+                    __nv_bfloat16* a, __nv_bfloat16* save, float* part, cudaStream_t st) {
+  const int T = c->T, H = c->H, F = c->F;
+  if (T <= SKINNY_T) {
+    FFN_RC((skinny::launch<skinny::Bf16, true>(
+        skinny_params(T, F, H, Wg, Wu, nullptr, nullptr, x, nullptr, a, nullptr, save), st, false)));
+    return skinny::launch<skinny::Bf16, false>(
+        skinny_params(T, H, F, Wd, nullptr, nullptr, nullptr, a, nullptr, y, nullptr, nullptr), st, true);
+  }
+  FFN_RC(gateup(T, H, F, x, Wg, Wu, a, save, part, st, false));
+  return down(T, H, F, a, Wd, y, part, st, true);
+}
+
+static int fwd_mxfp8(const moe_ffn_config* c, const void* x, const uint8_t* x_sf, const void* Wg, const void* Wu,
+                     const void* Wd, const uint8_t* Wg_sf, const uint8_t* Wu_sf, const uint8_t* Wd_sf, void* y,
+                     const FwdWs& w, cudaStream_t st) {
+  const int T = c->T, H = c->H, F = c->F;
+  const bool quant = x_sf == nullptr;
+  if (quant) {
+    FFN_RC(moe_impl::quantize_mxfp8(x, T, H, w.xq, w.xq_sf, st));
+    x = w.xq;
+    x_sf = w.xq_sf;
+  }
+  if (T <= SKINNY_T) {
+    FFN_RC((skinny::launch<skinny::Mx, true>(
+        skinny_params(T, F, H, Wg, Wu, Wg_sf, Wu_sf, x, x_sf, w.aq, w.aq_sf, nullptr), st, quant)));
+    return skinny::launch<skinny::Mx, false>(
+        skinny_params(T, H, F, Wd, nullptr, Wd_sf, nullptr, w.aq, w.aq_sf, y, nullptr, nullptr), st, true);
+  }
+  FFN_RC(moe_impl::fill_offsets2(w.off, T, st));
+  FFN_RC(moe_impl::gemm_gateup_mx(T, 1, H, F, x, x_sf, Wg, Wg_sf, Wu, Wu_sf, w.off, nullptr, w.aq, w.aq_sf, nullptr,
+                                  st));
+  return moe_impl::gemm_down_mx(T, 1, H, F, w.aq, w.aq_sf, Wd, Wd_sf, w.off, y, st);
+}
+
+}  // namespace ffn
+
+extern "C" size_t moe_ffn_workspace_size(const moe_ffn_config* cfg) {
+  if (ffn::check_cfg(cfg)) return 0;
+  ffn::FwdWs w;
+  return ffn::carve_fwd(nullptr, cfg, &w);
+}
+
+extern "C" size_t moe_ffn_saved_size(const moe_ffn_config* cfg) {
+  if (ffn::check_cfg(cfg) || cfg->dtype != MOE_DT_BF16) return 0;
+  ffn::Saved s;
+  return ffn::carve_saved(nullptr, cfg, &s);
+}
+
+extern "C" size_t moe_ffn_bwd_workspace_size(const moe_ffn_config* cfg) {
+  if (ffn::check_cfg(cfg) || cfg->dtype != MOE_DT_BF16) return 0;
+  ffn::BwdWs w;
+  return ffn::carve_bwd(nullptr, cfg, &w);
+}
+
+extern "C" int moe_ffn_fwd(const moe_ffn_config* cfg, const void* x, const uint8_t* x_sf, const void* W_g,
+                           const void* W_u, const void* W_d, const uint8_t* W_g_sf, const uint8_t* W_u_sf,
+                           const uint8_t* W_d_sf, void* y, void* saved, void* ws, size_t ws_bytes, void* stream) {
+  using namespace ffn;
+  FFN_RC(check_cfg(cfg));
+  if (!x || !W_g || !W_u || !W_d || !y) return MOE_ERR_INVALID_ARG;
+  const bool mx = cfg->dtype == MOE_DT_MXFP8;
+  if (mx ? (!W_g_sf || !W_u_sf || !W_d_sf) : (x_sf || W_g_sf || W_u_sf || W_d_sf)) return MOE_ERR_INVALID_ARG;
+  if ((cfg->save_for_bwd != 0) != (saved != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!a16(x) || !a16(W_g) || !a16(W_u) || !a16(W_d) || !a16(y) || !a16(saved) || !a16(ws) || !a4(x_sf) ||
+      !a4(W_g_sf) || !a4(W_u_sf) || !a4(W_d_sf))
+    return MOE_ERR_ALIGNMENT;
+  FwdWs w;
+  const size_t need = carve_fwd(nullptr, cfg, &w);
+  if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  carve_fwd(ws, cfg, &w);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (mx) return fwd_mxfp8(cfg, x, x_sf, W_g, W_u, W_d, W_g_sf, W_u_sf, W_d_sf, y, w, st);
+  Saved s{};
+  if (saved) carve_saved(saved, cfg, &s);
+  return fwd_bf16(cfg, x, W_g, W_u, W_d, y, saved ? s.a : w.a, s.gateup, w.part, st);
+}
+
+extern "C" int moe_ffn_bwd(const moe_ffn_config* cfg, const void* dY, const void* x, const void* W_g, const void* W_u,
+                           const void* W_d, const void* saved, void* dX, void* dW_g, void* dW_u, void* dW_d, void* ws,
+                           size_t ws_bytes, void* stream) {
+  using namespace ffn;
+  FFN_RC(check_cfg(cfg));
+  if (cfg->dtype != MOE_DT_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!cfg->save_for_bwd || !dY || !W_d || !saved) return MOE_ERR_INVALID_ARG;
+  if ((dW_g == nullptr) != (dW_u == nullptr) || (!dX && !dW_g && !dW_d)) return MOE_ERR_INVALID_ARG;
+  if ((dX && (!W_g || !W_u)) || (dW_g && !x)) return MOE_ERR_INVALID_ARG;
+  if (!a16(dY) || !a16(x) || !a16(W_g) || !a16(W_u) || !a16(W_d) || !a16(saved) || !a16(dX) || !a16(dW_g) ||
+      !a16(dW_u) || !a16(dW_d) || !a16(ws))
+    return MOE_ERR_ALIGNMENT;
+  BwdWs w;
+  if (!ws || ws_bytes < carve_bwd(nullptr, cfg, &w)) return MOE_ERR_WORKSPACE;
+  carve_bwd(ws, cfg, &w);
+  Saved s;
+  carve_saved(const_cast<void*>(saved), cfg, &s);
+  const int T = cfg->T, H = cfg->H, F = cfg->F;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  bool dep = false;
+  if (dX || dW_g) {
+    FFN_RC(dgrad_act(T, H, F, dY, W_d, s.gateup, w.dgu, w.part, st, dep));
+    dep = true;
+  }
+  if (dW_d) {
+    FFN_RC(wgrad(T, H, F, dY, nullptr, H, s.a, dW_d, nullptr, w.part, st, dep));
+    dep = true;
+  }
+  if (dX) FFN_RC(dgrad_x(T, H, F, w.dgu, W_g, W_u, dX, w.part, st, dep));
+  if (dW_g) FFN_RC(wgrad(T, F, H, w.dgu, w.dgu + F, 2LL * F, x, dW_g, dW_u, w.part, st, true));
+  return MOE_OK;
+}
