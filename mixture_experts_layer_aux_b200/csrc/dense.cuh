@@ -22,6 +22,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "swiglu.cuh"
 
 namespace dense {
 
@@ -125,19 +126,6 @@ MOE_DEV Origin origin(const Params& p, int tile) {
   o.rows = min(BM, p.M - o.m0);
   o.cols = min(Cfg<OP>::N_STEP, p.N - o.n0);
   return o;
-}
-
-MOE_DEV float silu_exact(float z, float& s) {
-  s = 1.0f / (1.0f + __expf(-z));
-  return z * s;
-}
-
-// SwiGLU backward of one element: v = d a, z = gate, u = up.
-MOE_DEV void swiglu_bwd(float v, float z, float u, float& dg, float& du) {
-  float s;
-  const float sl = silu_exact(z, s);
-  dg = v * u * s * (1.f + z * (1.f - s));
-  du = v * sl;
 }
 
 // 32 bf16 of each of the warp's 32 rows (16 words per lane, lane = row) to dst (row-contiguous through the
@@ -385,7 +373,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
             store_rows(stg, w, sv + p.N, ld2, rows, cols);
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) g[i] = silu_f(g[i]) * u[i];
+          for (int i = 0; i < 32; ++i) g[i] = swiglu::act(g[i], u[i]);
           pack32(g, w);
           store_rows(stg, w, p.C + row0 * p.ldc + o.n0 + c, p.ldc, rows, cols);
         }
@@ -405,8 +393,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float g0, u0, g1, u1;
-            swiglu_bwd(v[2 * i], word_lo(zg[i]), word_lo(zu[i]), g0, u0);
-            swiglu_bwd(v[2 * i + 1], word_hi(zg[i]), word_hi(zu[i]), g1, u1);
+            swiglu::grad(v[2 * i], word_lo(zg[i]), word_lo(zu[i]), g0, u0);
+            swiglu::grad(v[2 * i + 1], word_hi(zg[i]), word_hi(zu[i]), g1, u1);
             zg[i] = pack_bf16x2(g0, g1);
             zu[i] = pack_bf16x2(u0, u1);
           }
@@ -482,7 +470,7 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
         *reinterpret_cast<uint4*>(sv + p.N) = pack(u);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = silu_f(v[j]) * u[j];
+      for (int j = 0; j < 8; ++j) v[j] = swiglu::act(v[j], u[j]);
       *reinterpret_cast<uint4*>(p.C + row * p.ldc + o.n0 + c) = pack(v);
     } else if constexpr (OP == OP_DGRAD_ACT) {
       const __nv_bfloat16* src = p.gateup + row * 2LL * p.N + o.n0 + c;
@@ -490,7 +478,7 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
       unpack_bf16x8(*reinterpret_cast<const uint4*>(src), zg);
       unpack_bf16x8(*reinterpret_cast<const uint4*>(src + p.N), zu);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) swiglu_bwd(v[j], zg[j], zu[j], v[j], u[j]);
+      for (int j = 0; j < 8; ++j) swiglu::grad(v[j], zg[j], zu[j], v[j], u[j]);
       __nv_bfloat16* dst = p.C + row * 2LL * p.N + o.n0 + c;
       *reinterpret_cast<uint4*>(dst) = pack(v);
       *reinterpret_cast<uint4*>(dst + p.N) = pack(u);

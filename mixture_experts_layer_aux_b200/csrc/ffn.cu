@@ -1,7 +1,7 @@
 // ffn.cu -- the gated feed-forward block y = W_d (silu(W_g x) * (W_u x)) on its
 // own (a dense layer of the stack, or a shared expert), forward in bf16 and
 // MXFP8 and backward in bf16.
-//   few tokens    the streaming kernels of skinny.cuh (two launches; MXFP8 from
+//   few tokens    the streaming kernels of stream.cuh (two launches; MXFP8 from
 //                 a bf16 x: three);
 //   more, bf16    the dense tensor-core kernel of dense.cuh;
 //   more, MXFP8   the block-scaled grouped GEMM as one group.
@@ -11,7 +11,7 @@
 #include "common.cuh"
 #include "dense.cuh"
 #include "layout.h"
-#include "skinny.cuh"
+#include "stream.cuh"
 
 namespace moe_impl {
 int gemm_gateup_mx(int rows, int groups, int H, int F, const void* A, const uint8_t* A_sf, const void* Wg,
@@ -26,7 +26,7 @@ namespace ffn {
 using dense::Params;
 
 // Tokens up to which the streaming kernels are taken.
-constexpr int SKINNY_T = skinny::MAX_T;
+constexpr int STREAM_T = stream::MAX_T;
 
 #define FFN_RC(x)         \
   do {                    \
@@ -69,7 +69,7 @@ static size_t carve_fwd(void* ws, const moe_ffn_config* c, FwdWs* w) {
     w->off = cv.take<int32_t>(2);
   } else {
     if (!c->save_for_bwd) w->a = cv.take<__nv_bfloat16>(T * F);
-    if (c->T > SKINNY_T) w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
+    if (c->T > STREAM_T) w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
   }
   return cv.used;
 }
@@ -163,33 +163,62 @@ static int wgrad(int T, int M, int N, const void* dO, const void* dO2, long long
   return dense::launch<dense::OP_WGRAD>(p, st, dep);
 }
 
-static skinny::Params skinny_params(int T, int N, int K, const void* W0, const void* W1, const uint8_t* sf0,
-                                    const uint8_t* sf1, const void* x, const uint8_t* x_sf, void* out,
-                                    uint8_t* out_sf, void* save) {
-  skinny::Params p{};
-  p.W0 = static_cast<const uint8_t*>(W0);
-  p.W1 = static_cast<const uint8_t*>(W1);
+// One product of the streaming path: W1 for gate/up, scales for MXFP8.
+template <bool MX, bool GATEUP>
+static int stream_gemm(int T, int N, int K, const void* W0, const void* W1, const uint8_t* sf0, const uint8_t* sf1,
+                       const void* x, const uint8_t* x_sf, void* out, uint8_t* out_sf, void* save, cudaStream_t st,
+                       bool dep, const void* W_next = nullptr) {
+  stream::Params p = stream::plan<MX, GATEUP>(T, N, K);
+  if (GATEUP && !stream::plan_next<MX>(p, W_next)) return MOE_ERR_CUDA;
+  if (!stream::encode_map<MX>(&p.tmW0, p, W0, N, p.r) || (GATEUP && !stream::encode_map<MX>(&p.tmW1, p, W1, N, p.r)) ||
+      !stream::encode_map<MX>(&p.tmX, p, x, T, T))
+    return MOE_ERR_CUDA;
   p.sf0 = sf0;
   p.sf1 = sf1;
-  p.x = static_cast<const uint8_t*>(x);
   p.x_sf = x_sf;
   p.out = out;
   p.out_sf = out_sf;
   p.save = static_cast<__nv_bfloat16*>(save);
-  p.T = T;
-  p.N = N;
-  p.K = K;
-  return p;
+  return stream::launch<MX, GATEUP>(p, st, dep);
+}
+
+// x [T, H] bf16 -> MXFP8 for the streaming path: a thread takes 8 elements, four lanes a 1x32 block. The kernel
+// behind it may start at once (its weights do not depend on x).
+__global__ void __launch_bounds__(256) quantize_kernel(const __nv_bfloat16* __restrict__ x, long long n8,
+                                                       uint8_t* __restrict__ q, uint8_t* __restrict__ sf) {
+  griddep_launch_dependents();
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const bool ok = i < n8;  // n8 % 4 == 0: the lanes of a block are all in or all out
+  float v[8];
+  unpack_bf16x8(ok ? *reinterpret_cast<const uint4*>(x + 8 * i) : make_uint4(0, 0, 0, 0), v);
+  float am = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(v[j]));
+  am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+  am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+  const uint8_t sb = ggmx::mx_scale_byte(am);
+  const float inv = ggmx::mx_inv_scale(sb);
+  uint32_t w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    w[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * k] * inv, v[4 * k + 1] * inv), __NV_SATFINITE,
+                                              __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * k + 2] * inv, v[4 * k + 3] * inv), __NV_SATFINITE,
+                                              __NV_E4M3)
+               << 16;
+  if (!ok) return;
+  reinterpret_cast<uint2*>(q)[i] = make_uint2(w[0], w[1]);
+  if ((threadIdx.x & 3) == 0) sf[i >> 2] = sb;
 }
 
 static int fwd_bf16(const moe_ffn_config* c, const void* x, const void* Wg, const void* Wu, const void* Wd, void* y,
                     __nv_bfloat16* a, __nv_bfloat16* save, float* part, cudaStream_t st) {
   const int T = c->T, H = c->H, F = c->F;
-  if (T <= SKINNY_T) {
-    FFN_RC((skinny::launch<skinny::Bf16, true>(
-        skinny_params(T, F, H, Wg, Wu, nullptr, nullptr, x, nullptr, a, nullptr, save), st, false)));
-    return skinny::launch<skinny::Bf16, false>(
-        skinny_params(T, H, F, Wd, nullptr, nullptr, nullptr, a, nullptr, y, nullptr, nullptr), st, true);
+  if (T <= STREAM_T) {
+    FFN_RC((stream_gemm<false, true>(T, F, H, Wg, Wu, nullptr, nullptr, x, nullptr, a, nullptr, save, st, false,
+                                     Wd)));
+    return stream_gemm<false, false>(T, H, F, Wd, nullptr, nullptr, nullptr, a, nullptr, y, nullptr, nullptr, st,
+                                     true);
   }
   FFN_RC(gateup(T, H, F, x, Wg, Wu, a, save, part, st, false));
   return down(T, H, F, a, Wd, y, part, st, true);
@@ -201,15 +230,22 @@ static int fwd_mxfp8(const moe_ffn_config* c, const void* x, const uint8_t* x_sf
   const int T = c->T, H = c->H, F = c->F;
   const bool quant = x_sf == nullptr;
   if (quant) {
-    FFN_RC(moe_impl::quantize_mxfp8(x, T, H, w.xq, w.xq_sf, st));
+    if (T <= STREAM_T) {
+      const long long n8 = (long long)T * H / 8;
+      quantize_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), n8, w.xq,
+                                                                   w.xq_sf);
+      MOE_CHECK_LAUNCH();
+    } else {
+      FFN_RC(moe_impl::quantize_mxfp8(x, T, H, w.xq, w.xq_sf, st));
+    }
     x = w.xq;
     x_sf = w.xq_sf;
   }
-  if (T <= SKINNY_T) {
-    FFN_RC((skinny::launch<skinny::Mx, true>(
-        skinny_params(T, F, H, Wg, Wu, Wg_sf, Wu_sf, x, x_sf, w.aq, w.aq_sf, nullptr), st, quant)));
-    return skinny::launch<skinny::Mx, false>(
-        skinny_params(T, H, F, Wd, nullptr, Wd_sf, nullptr, w.aq, w.aq_sf, y, nullptr, nullptr), st, true);
+  if (T <= STREAM_T) {
+    FFN_RC((stream_gemm<true, true>(T, F, H, Wg, Wu, Wg_sf, Wu_sf, x, x_sf, w.aq, w.aq_sf, nullptr, st, quant,
+                                    Wd)));
+    return stream_gemm<true, false>(T, H, F, Wd, nullptr, Wd_sf, nullptr, w.aq, w.aq_sf, y, nullptr, nullptr, st,
+                                    true);
   }
   FFN_RC(moe_impl::fill_offsets2(w.off, T, st));
   FFN_RC(moe_impl::gemm_gateup_mx(T, 1, H, F, x, x_sf, Wg, Wg_sf, Wu, Wu_sf, w.off, nullptr, w.aq, w.aq_sf, nullptr,

@@ -1,0 +1,755 @@
+// stream.cuh -- the gated feed-forward block for few tokens (one token of a
+// decoding step up to MAX_T), where the time is that of streaming the weights
+// through the SMs once.
+//
+// The product is taken transposed on the tensor cores: the weights are the M
+// side (128 rows of an MMA), the tokens the N side, so nothing is padded to 128
+// tokens. What would be the tile's height is free instead: a CTA owns
+// r = ceil(rows / SMs) weight rows (the height of its TMA boxes, any number up
+// to 128), so that every SM streams the same number of bytes, K is never split
+// over CTAs and no partial sums are exchanged.
+//   gate/up  r columns of F: r rows of W_g and r rows of W_u; the SwiGLU (MXFP8:
+//            and the 1x32 quantisation of the activation, r a multiple of 32)
+//            is the epilogue;
+//   down     r rows of W_d.
+// Where r is small, an MMA of 128 rows would be mostly empty and, at about 45
+// clocks whatever its N up to 16, set the pace instead of memory. So s blocks of
+// K (128 bytes per row each) are stacked: rows c r + i of the operand are K block
+// c of weight row i, rows c T + t of the other are block c of token t, and the
+// accumulator's diagonal blocks (c, c), added in the epilogue, are the result.
+// With 2 s r <= 128, W_u's rows follow W_g's in the same operand. The boxes are
+// three-dimensional (128 bytes x rows x s blocks): one copy per operand and
+// stage, since small copies cost as much as large ones (on B200 a stage of
+// 3.5 + 2 KB took 240 ns, whatever was done with it).
+// Operand rows that no box fills read whatever lies behind it in shared memory;
+// a row (column) of the accumulator depends on its own operand row alone, and
+// those are not stored.
+// Stages go through a ring of up to 95 KB, so that two CTAs fit on an SM: the
+// down kernel starts while the gate/up kernel ends (programmatic dependent
+// launch), and its first weights, which depend on nothing, are on their way
+// before it waits for the activation.
+//
+// Once the gate/up kernel's last weights are on their way, its producer asks
+// for the down kernel's to be brought into L2, so that memory stays busy while
+// the one ends and the other begins.
+//
+// Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer and TMEM owner
+// (MXFP8: warp 3 a second issuer; the rings then have an even number of stages,
+// so that a stage has one issuer, who sees each of its phases), warp 2 loader of the MXFP8 scales (natural [rows, K/32] layout -> the chunk
+// order of the tensor-memory copies, see gemm_mx.cuh), warps 4..11 epilogue
+// (TMEM lane quadrant w % 4, every other 16 tokens). Every wait is bounded
+// (MOE_WAIT_NS).
+#pragma once
+
+#include "common.cuh"
+#include "gemm_mx.cuh"
+#include "swiglu.cuh"
+
+namespace moe_host {
+// 3-D tiled map {inner, rows, blocks} with byte strides of rows and blocks, 128-byte swizzle, zero fill.
+bool encode_tmap_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
+                    uint64_t blocks, uint64_t row_stride, uint64_t block_stride, uint32_t box_inner,
+                    uint32_t box_rows, uint32_t box_blocks);
+}  // namespace moe_host
+
+namespace stream {
+
+constexpr int MAX_T = 64;
+constexpr int MAX_STAGES = 16;
+constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
+constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+// MMA issuers, each with accumulators of its own and every other stage: one thread's instructions (some 35 ns an MMA,
+// 60 a copy of scales or a commit) keep up with memory at 16 KB of bf16 per stage, not at MXFP8 with its scales (8
+// tokens, H = 7168, F = 2048: 28.7 us with one, 26.8 with two; bf16 is 2 us faster with one and an odd stage more).
+constexpr int issuers(bool mx) { return mx ? 2 : 1; }
+constexpr int ROW_BYTES = 128;            // K bytes of a stage row (64 bf16 or 128 e4m3)
+constexpr int OPERAND_BYTES = 128 * ROW_BYTES;  // what an MMA reads of its weight operand, filled or not
+constexpr int MAX_N = 224;                // s T at most (two issuers' accumulators and the scales in 512 TMEM columns)
+constexpr int SF_SLOTS = 16;              // MXFP8: stages of scales in shared memory, on a ring of their own
+constexpr int SF_SLOT_COLS = 16;          // scale columns of a stage in TMEM (W0, W1: 128 rows; x: 256 rows)
+constexpr int MAX_CLUSTER = 4;            // CTAs that share a tile, each taking a part of K
+constexpr int BAR_BYTES = 1024;
+// Bytes of the ring. A CTA with little to stream (up to SHORT_BYTES in all) leaves room for one of the other kernel
+// on its SM, which then starts while it runs; with much to stream, bytes in flight count: about 2 us of latency at
+// 46 GB/s per SM (T = 1, H = 4096, F = 14336 bf16: 65 us with the large rings, 70 with the shared ones; MXFP8
+// H = 7168, F = 2048: 32.4 and 28.7).
+constexpr int RING_GATEUP = 116 * 1024, RING_DOWN = 100 * 1024, RING_ALONE = 200 * 1024;
+constexpr int SHORT_BYTES = 512 * 1024;
+constexpr int SMEM_FIXED = 1024 + BAR_BYTES;
+
+struct __align__(64) Params {
+  CUtensorMap tmW0, tmW1, tmX;
+  CUtensorMap tmNext;               // gate/up: the down kernel's W0, its rows per tile, blocks per stage, tiles, and
+  int next_r, next_s, next_tiles;   // the stages to bring into L2 (from, to)
+  int next_from, next_to;
+  const uint8_t *sf0, *sf1, *x_sf;  // MXFP8 scales, [rows, K/32]
+  void* out;                        // gate/up: [T, N] bf16, or e4m3 codes; down: [T, N] bf16
+  uint8_t* out_sf;                  // MXFP8 gate/up: [T, N/32]
+  __nv_bfloat16* save;              // bf16 gate/up: gate | up [T, 2N], or NULL
+  int T, N, K;                      // tokens, weight rows, reduction length
+  int r, s;                         // weight rows per tile, K blocks per stage
+  int KB, KS;                       // K blocks (128 bytes), stages of s blocks
+  int w_rows;                       // s r rounded up to 8: operand rows of one weight
+  int mma_n;                        // s T rounded up to 16
+  int z;                            // tensor maps are cut along K (K a whole number of blocks; else s = 1)
+  int tiles;
+  int stages, stage_bytes;
+  int ring_bytes;                   // the stages, and what the last one's operands read past it
+  int sf_w1, sf_x, sf_bytes;        // MXFP8: offsets of W1's and x's chunks in a slot of scales, and its size
+  int cs;                           // CTAs per tile (a cluster, each with a part of K), MXFP8 gate/up
+  int acc_cols, acc_bufs, tmem_cols;  // TMEM: columns of one accumulator set, sets, allocation
+  int merged;                       // gate/up: both weights in one operand
+  int staged;                       // the epilogue goes through shared memory (s > 1, merged or cs > 1)
+  int* status;
+};
+
+static_assert(SF_SLOTS % issuers(true) == 0, "a slot of scales has one issuer");
+
+// Instruction descriptors: bf16 (common.cuh) and MXFP8 (gemm_mx.cuh) with a run-time N.
+template <bool MX>
+MOE_DEV uint32_t idesc(int N, int q) {
+  return MX ? ggmx::idesc_mx(128, N, q) : idesc_bf16(128, N, 0, 0);
+}
+
+MOE_DEV void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 3-D tile: x (elements), row, K block.
+MOE_DEV void tma_load_3d(void* smem_dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+MOE_DEV void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+MOE_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same shared-memory address in CTA `rank` of the cluster, as a generic pointer.
+MOE_DEV const void* cluster_ptr(const void* p, uint32_t rank) {
+  uint64_t r;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
+  return reinterpret_cast<const void*>(r);
+}
+
+// 4-byte asynchronous copy global -> shared; bytes 0: the destination is zeroed, nothing is read.
+MOE_DEV void cp_async4(void* smem_dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(bytes)
+               : "memory");
+}
+// Arrives on `bar` (counted among its expected arrivals) once this thread's copies so far have landed.
+MOE_DEV void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+MOE_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Where an operand row's scale word lies in its chunks.
+MOE_DEV int chunk_offset(int row) { return 512 * (row >> 7) + 16 * (row & 31) + 4 * ((row >> 5) & 3); }
+
+// Quantises one element per lane of a 32-lane block (fp32 a; NaN does not enter the maximum, as fmaxf).
+MOE_DEV uint8_t quant_lane(float a, uint8_t& sb) {
+  const float am = fmaxf(fabsf(a), 0.f);
+  sb = ggmx::mx_scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(am))));
+  return __nv_cvt_float_to_fp8(a * ggmx::mx_inv_scale(sb), __NV_SATFINITE, __NV_E4M3);
+}
+
+template <bool MX, bool GATEUP>
+__global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_constant__ Params p) {
+  constexpr int ISSUERS = issuers(MX);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sf_ring = ring + p.ring_bytes;
+  uint8_t* bar_area = sf_ring + (MX ? SF_SLOTS * p.sf_bytes : 0);
+  uint64_t* full = reinterpret_cast<uint64_t*>(bar_area);
+  uint64_t* empty = full + MAX_STAGES;
+  uint64_t* sfull = empty + MAX_STAGES;
+  uint64_t* sempty = sfull + SF_SLOTS;
+  uint64_t* tfull = sempty + SF_SLOTS;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* staged = tempty + 2;
+  uint64_t* drain = staged + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + ISSUERS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w_bytes = p.w_rows * ROW_BYTES;
+  const int x_off = (GATEUP ? 2 : 1) * w_bytes;
+  // MXFP8 gate/up: cs consecutive CTAs (a cluster) share a tile; this one takes the stages [ks0, ks1) of K
+  constexpr bool CLUSTER = MX && GATEUP;
+  const int rank = CLUSTER ? (int)blockIdx.x % p.cs : 0;
+  const int tile0 = CLUSTER ? (int)blockIdx.x / p.cs : (int)blockIdx.x;
+  const int tile_step = CLUSTER ? (int)gridDim.x / p.cs : (int)gridDim.x;
+  const int ks0 = CLUSTER ? rank * p.KS / p.cs : 0, ks1 = CLUSTER ? (rank + 1) * p.KS / p.cs : p.KS;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; MX && i < SF_SLOTS; ++i) {
+      mbar_init(&sfull[i], 32);  // the loader's lanes
+      mbar_init(&sempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], ISSUERS);
+      mbar_init(&tempty[i], EPI_WARPS);
+    }
+    mbar_init(staged, EPI_WARPS);
+    for (int i = 0; i < ISSUERS; ++i) mbar_init(&drain[i], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 32 * 3) {
+    tma_prefetch_desc(&p.tmW0);
+    if (GATEUP) tma_prefetch_desc(&p.tmW1);
+    tma_prefetch_desc(&p.tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, p.tmem_cols);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_launch_dependents();
+
+  // Staged epilogue, from shared memory on: adds the parts of every element, in the order of K, and writes it. A
+  // warp takes 32 columns of one token; the CTAs of a cluster divide the tokens among themselves.
+  const auto finish = [&](int t) {
+    const int n0 = t * p.r, rows = min(p.r, p.N - n0), cg = (p.r + 31) / 32;
+    const int first = (warp - EPI_WARP0) * (CLUSTER ? p.cs : 1) + rank, step = EPI_WARPS * (CLUSTER ? p.cs : 1);
+    for (int e = first; e < p.T * cg; e += step) {
+      const int tok = e / cg, f = 32 * (e - tok * cg) + lane;
+      const bool ok = f < rows;
+      float g = 0.f, u = 0.f;
+      if (ok)
+        for (int k = 0; k < (CLUSTER ? p.cs : 1); ++k) {
+          const float* st = reinterpret_cast<const float*>(CLUSTER && p.cs > 1 ? cluster_ptr(ring, k) : ring);
+          for (int c = 0; c < p.s; ++c) {
+            g += st[(c * p.T + tok) * p.r + f];
+            if (GATEUP) u += st[((p.s + c) * p.T + tok) * p.r + f];
+          }
+        }
+      const float a = GATEUP ? swiglu::act(g, u) : g;
+      const long long o = (long long)tok * p.N + n0 + f;
+      if (MX && GATEUP) {
+        uint8_t sb;
+        const uint8_t code = quant_lane(a, sb);
+        if (ok) {
+          static_cast<uint8_t*>(p.out)[o] = code;
+          if (lane == 0) p.out_sf[o >> 5] = sb;
+        }
+      } else if (ok) {
+        static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a);
+        if (GATEUP && p.save) {
+          __nv_bfloat16* sv = p.save + (long long)tok * 2 * p.N + n0 + f;
+          sv[0] = __float2bfloat16_rn(g);
+          sv[p.N] = __float2bfloat16_rn(u);
+        }
+      }
+    }
+  };
+
+  bool aborted = false;
+  if (warp == 0) {
+    // ======================= TMA producer
+    if (lane == 0) {
+      const uint32_t tx = (uint32_t)(((GATEUP ? 2 : 1) * p.r + p.T) * p.s * ROW_BYTES);
+      const int kstep = MX ? 128 : 64;
+      int stage = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_par = 0;
+      // the ks-th stage of K: coordinate along K, or the block's number where the maps are cut along it
+      const auto load = [&](const CUtensorMap* m, int row, int ks, uint8_t* dst, uint64_t* bar) {
+        const int kb = ks * p.s;
+        tma_load_3d(dst, m, p.z ? 0 : kb * kstep, row, p.z ? kb : 0, bar);
+      };
+      const auto load_w = [&](int t, int ks, int st) {
+        uint8_t* b = ring + st * p.stage_bytes;
+        load(&p.tmW0, t * p.r, ks, b, &full[st]);
+        if (GATEUP) load(&p.tmW1, t * p.r, ks, b + w_bytes, &full[st]);
+      };
+      // the first weights, before the wait for the kernel that makes x
+      const int ahead = min(p.stages, ks1 - ks0);
+      for (int st = 0; st < ahead; ++st) {
+        mbar_arrive_expect_tx(&full[st], tx);
+        issued_mask |= 1u << st;
+        load_w(tile0, ks0 + st, st);
+      }
+      griddep_wait();
+      for (int t = tile0; t < p.tiles && !aborted; t += tile_step) {
+        for (int ks = ks0; ks < ks1; ++ks) {
+          const bool early = t == tile0 && ks < ks0 + ahead;
+          if (!early) {
+            if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) {
+              aborted = true;
+              break;
+            }
+            mbar_arrive_expect_tx(&full[stage], tx);
+            issued_mask |= 1u << stage;
+            issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+            load_w(t, ks, stage);
+          }
+          load(&p.tmX, 0, ks, ring + stage * p.stage_bytes + x_off, &full[stage]);
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (GATEUP)
+        for (int ks = p.next_from; ks < p.next_to && !aborted; ++ks)
+          for (int t = blockIdx.x; t < p.next_tiles; t += gridDim.x)
+            tma_prefetch_3d(&p.tmNext, 0, t * p.next_r, ks * p.next_s);
+      if (*abort_flag) {
+        // every TMA this thread issued must land before the CTA exits
+        for (int i = 0; i < p.stages; ++i)
+          if (issued_mask & (1u << i)) {
+            const uint32_t par = (issued_par >> i) & 1u;
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(&full[i], par) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
+            }
+          }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 || (ISSUERS == 2 && warp == 3)) {
+    // ======================= MMA issuers: single threads, whose instructions set the pace, so everything that does
+    // not change from stage to stage is kept: descriptors are a constant plus the address / 16
+    if (lane == 0) {
+      const int me = warp >> 1;
+      const bool two = GATEUP && !p.merged;
+      const uint64_t desc0 = smem_desc_sw128(0, 16, 1024) + (smem_u32(ring) >> 4);
+      const uint64_t sdesc0 = ggmx::sf_desc(0) + (smem_u32(sf_ring) >> 4);
+      const uint32_t stage16 = p.stage_bytes >> 4, w16 = w_bytes >> 4, x16 = x_off >> 4;
+      int slot = 0;
+      uint32_t sphase = 0;
+      const uint32_t sf_tmem = tmem_base + p.acc_bufs * ISSUERS * p.acc_cols + me * 2 * SF_SLOT_COLS;
+      uint32_t id[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) id[q] = idesc<MX>(p.mma_n, q);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      for (int t = tile0; t < p.tiles && !aborted; t += tile_step) {
+        if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
+          aborted = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d0 = tmem_base + (acc * ISSUERS + me) * p.acc_cols, d1 = d0 + p.mma_n;
+        bool first = true, slot2 = false;
+        uint64_t ad = desc0 + stage * stage16;
+        for (int ks = ks0; ks < ks1; ++ks) {
+          if (ISSUERS == 2 && (stage & 1) != me) {  // the other issuer's
+            if (MX && ++slot == SF_SLOTS) {
+              slot = 0;
+              sphase ^= 1;
+            }
+            ad += stage16;
+            if (++stage == p.stages) {
+              stage = 0;
+              phase ^= 1;
+              ad = desc0;
+            }
+            continue;
+          }
+          if ((MX && !mbar_wait(&sfull[slot], sphase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) ||
+              !mbar_wait(&full[stage], phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t bd = ad + x16;
+          // scale slots of TMEM alternate: the copies of a stage follow, in issue order, the MMAs that read
+          // the slot two stages ago
+          const uint32_t sc = sf_tmem + (slot2 ? SF_SLOT_COLS : 0);
+          slot2 = !slot2;
+          if (MX) {
+            fence_proxy_async_smem();  // the scales were written by ordinary copies, and are read by tcgen05.cp
+            const uint64_t sd = sdesc0 + slot * (p.sf_bytes >> 4), sx = sd + (p.sf_x >> 4);
+            ggmx::tmem_cp_32x128b_x4(sc, sd);
+            if (two) ggmx::tmem_cp_32x128b_x4(sc + 4, sd + (512 >> 4));
+            ggmx::tmem_cp_32x128b_x4(sc + 8, sx);
+            if (p.mma_n > 128) ggmx::tmem_cp_32x128b_x4(sc + 12, sx + (512 >> 4));
+          }
+          const auto mma = [&](uint32_t d, uint64_t a, uint32_t sa, int q) {
+            const uint32_t on = !first || q != 0 ? 1u : 0u;
+            if (MX)
+              ggmx::mma_mxf8(d, a + 2 * q, bd + 2 * q, id[q], sa | ((uint32_t)q << 30), (sc + 8) | ((uint32_t)q << 30),
+                             on);
+            else
+              mma_bf16(d, a + 2 * q, bd + 2 * q, id[q], on);
+          };
+          if (two) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              mma(d0, ad, sc, q);
+              mma(d1, ad + w16, sc + 4, q);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mma(d0, ad, sc, q);
+          }
+          first = false;
+          mma_commit(&empty[stage]);
+          if (MX) {
+            mma_commit(&sempty[slot]);
+            if (++slot == SF_SLOTS) {
+              slot = 0;
+              sphase ^= 1;
+            }
+          }
+          ad += stage16;
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1;
+            ad = desc0;
+          }
+        }
+        if (aborted) break;
+        mma_commit(&tfull[acc]);
+        if (++acc == p.acc_bufs) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+      if (*abort_flag) {
+        // wait for every MMA already issued before TMEM is released
+        mma_commit(&drain[me]);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&drain[me], 0) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ======================= MXFP8 scales. A chunk holds 128 operand rows: row 32 i + l in bytes 16 l + 4 i .. + 3,
+    // one byte per 1x32 block of a K block. Every word goes from its place in the natural layout to its place in the
+    // chunk by a 4-byte asynchronous copy whose completion arrives on its slot's barrier. Sixteen stages of scales
+    // are in flight (through registers, with the next four K blocks loaded ahead, the loads' latency set the pace:
+    // 32.8 us for 29 MB of gate/up weights; as deep as the operands' ring only, 22.6).
+    if constexpr (MX) {
+      const int kw = p.K / 32;  // scale bytes per row
+      // Lane l copies the words of operand rows l + 32 j: block c = row / r of weight row (token) row % r. A block
+      // past the end of K (of a last stage) or a row past the weights is zero-filled.
+      constexpr int WJ = 4, XJ = MAX_N / 32;
+      const uint8_t *w0[WJ], *xs[XJ];
+      int wc[WJ], wd[WJ], xc[XJ];
+      const long long w1 = GATEUP ? p.sf1 - p.sf0 : 0;
+      const auto rows = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < WJ; ++j) {
+          const int e = lane + 32 * j, c = (e >= p.r) + (e >= 2 * p.r) + (e >= 3 * p.r), i = e - c * p.r;  // s <= 4
+          const long long n = (long long)t * p.r + i;
+          w0[j] = p.sf0 + n * kw + 4 * c;
+          wc[j] = e < p.s * p.r && n < p.N ? c : 1 << 20;
+          wd[j] = p.merged ? chunk_offset(e + p.w_rows) : p.sf_w1 + chunk_offset(e);
+        }
+      };
+      rows(tile0);
+#pragma unroll
+      for (int j = 0; j < XJ; ++j) {
+        const int e = lane + 32 * j, c = (e >= p.T) + (e >= 2 * p.T) + (e >= 3 * p.T);
+        xs[j] = p.x_sf + (long long)(e - c * p.T) * kw + 4 * c;
+        xc[j] = c;
+      }
+      const auto weights = [&](int ks, int st) {
+        uint8_t* sf = sf_ring + st * p.sf_bytes;
+#pragma unroll
+        for (int j = 0; j < WJ; ++j) {
+          if (lane + 32 * j >= p.s * p.r) continue;
+          const bool ok = ks * p.s + wc[j] < p.KB;
+          const uint8_t* src = ok ? w0[j] + 4 * ks * p.s : p.sf0;
+          cp_async4(sf + 16 * lane + 4 * j, src, ok ? 4 : 0);
+          if (GATEUP) cp_async4(sf + wd[j], ok ? src + w1 : p.sf1, ok ? 4 : 0);
+        }
+      };
+      const auto tokens = [&](int ks, int st) {
+        uint8_t* sf = sf_ring + st * p.sf_bytes + p.sf_x;
+#pragma unroll
+        for (int j = 0; j < XJ; ++j) {
+          if (lane + 32 * j >= p.s * p.T) continue;
+          const bool ok = ks * p.s + xc[j] < p.KB;
+          cp_async4(sf + 512 * (j >> 2) + 16 * lane + 4 * (j & 3), ok ? xs[j] + 4 * ks * p.s : p.x_sf, ok ? 4 : 0);
+        }
+        cp_async_arrive(&sfull[st]);
+      };
+      const int ahead = min(SF_SLOTS, ks1 - ks0);
+      for (int st = 0; st < ahead; ++st) weights(ks0 + st, st);
+      griddep_wait();
+      int slot = 0;
+      uint32_t phase = 0;
+      for (int t = tile0; t < p.tiles && !aborted; t += tile_step) {
+        if (t != tile0) rows(t);
+        for (int ks = ks0; ks < ks1; ++ks) {
+          if (t != tile0 || ks >= ks0 + ahead) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&sempty[slot], phase ^ 1, abort_flag, p.status,
+                                                   DEV_WAIT_TIMEOUT_PRODUCER))) {
+              aborted = true;
+              break;
+            }
+            weights(ks, slot);
+          }
+          tokens(ks, slot);
+          if (++slot == SF_SLOTS) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      cp_async_wait_all();  // (after an abort) no copy outlives the CTA
+    }
+  } else if (warp >= EPI_WARP0) {
+    // ======================= epilogue: TMEM lanes 32 q .. 32 q + 31 = rows of the tile, columns = tokens
+    griddep_wait();  // what the kernel before this one still reads may be what is written here
+    const int q = warp & 3, h = (warp - EPI_WARP0) >> 2;
+    const int row = 32 * q + lane;
+    int acc = 0, iter = 0;
+    uint32_t acc_phase = 0;
+    for (int t = tile0; t < p.tiles && !aborted; t += tile_step) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_EPILOGUE))) {
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + acc * ISSUERS * p.acc_cols;
+      // with a single stage of K, only its issuer's accumulator holds something
+      const bool both = ISSUERS == 2 && ks1 - ks0 > 1;
+      const uint32_t tb1 = ISSUERS == 1 || both || !(iter++ & 1) ? tb : tb + p.acc_cols;
+      const int n0 = t * p.r;
+      const int rows = min(p.r, p.N - n0);
+      if (p.staged) {
+        // the parts of one element are on different lanes and columns: through shared memory (the ring, whose
+        // stages have all been read: a staged launch has one tile per CTA), fp32 [part][token][r], the parts
+        // being the K blocks of a stage, of W0 and then of W1
+        float* st = reinterpret_cast<float*>(ring);
+        for (int c = 0; c < p.s; ++c) {
+          for (int m = 0; m < (GATEUP ? 2 : 1); ++m) {
+            // this lane's operand row, as an index into block c of weight m
+            const int i = row - m * p.w_rows - c * p.r;
+            const bool mine = i >= 0 && i < p.r;
+            if (!__any_sync(0xffffffffu, mine)) continue;
+            const uint32_t col = tb1 + c * p.T;
+            for (int j = 16 * h; j < p.T; j += 32) {
+              float v[16], v2[16];
+              tmem_ld16(col + j, v);
+              if (both) tmem_ld16(col + p.acc_cols + j, v2);
+              tmem_ld_wait();
+              if (both)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] += v2[k];
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (mine && j + k < p.T) st[((m * p.s + c) * p.T + j + k) * p.r + i] = v[k];
+            }
+          }
+        }
+        if (CLUSTER && p.cs > 1) continue;  // finished below, with the other CTAs' parts
+        __syncwarp();
+        if (lane == 0) mbar_arrive(staged);
+        if (!__all_sync(0xffffffffu, mbar_wait(staged, 0, abort_flag, p.status, DEV_WAIT_TIMEOUT_EPILOGUE))) {
+          aborted = true;
+          break;
+        }
+        finish(t);
+      } else {
+        const bool ok = row < rows;
+        for (int c = 16 * h; c < p.T; c += 32) {
+          float v[16], u[16], v2[16], u2[16];
+          tmem_ld16(tb1 + c, v);
+          if (GATEUP) tmem_ld16(tb1 + p.mma_n + c, u);
+          if (both) {
+            tmem_ld16(tb + p.acc_cols + c, v2);
+            if (GATEUP) tmem_ld16(tb + p.acc_cols + p.mma_n + c, u2);
+          }
+          tmem_ld_wait();
+          if (both)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              v[i] += v2[i];
+              if (GATEUP) u[i] += u2[i];
+            }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c + i >= p.T) break;
+            const long long o = (long long)(c + i) * p.N + n0 + row;
+            if constexpr (GATEUP) {
+              const float a = swiglu::act(v[i], u[i]);
+              if (MX) {
+                uint8_t sb;
+                const uint8_t code = quant_lane(ok ? a : 0.f, sb);
+                if (ok) {
+                  static_cast<uint8_t*>(p.out)[o] = code;
+                  if (lane == 0) p.out_sf[o >> 5] = sb;
+                }
+              } else if (ok) {
+                static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a);
+                if (p.save) {
+                  __nv_bfloat16* sv = p.save + (long long)(c + i) * 2 * p.N + n0 + row;
+                  sv[0] = __float2bfloat16_rn(v[i]);
+                  sv[p.N] = __float2bfloat16_rn(u[i]);
+                }
+              }
+            } else if (ok) {
+              static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v[i]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[acc]);
+      if (++acc == p.acc_bufs) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+  }
+  if (CLUSTER && p.cs > 1) {
+    // every CTA's parts are in its shared memory; it stays until the others have read them
+    __syncwarp();
+    cluster_sync();
+    if (warp >= EPI_WARP0) finish(tile0);
+    __syncwarp();
+    cluster_sync();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+}
+
+// Geometry of a launch: rows per tile, K blocks per stage, stages, accumulators. The tensor maps follow from it
+// (boxes of 128 bytes x r rows, or T tokens, x s blocks).
+template <bool MX, bool GATEUP>
+Params plan(int T, int N, int K) {
+  constexpr int ISSUERS = issuers(MX);
+  Params p{};
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  const int kstep = MX ? 128 : 64;
+  p.KB = (K + kstep - 1) / kstep;
+  p.z = K % kstep == 0;
+  const int sms = moe_host::num_sms();
+  // equal tiles of at most 128 rows, in as few rounds over the SMs as that allows; the MXFP8 activation's blocks
+  // of 32 columns stay within a tile
+  const int unit = MX && GATEUP ? 32 : 8;
+  const int rounds = (N + 128 * sms - 1) / (128 * sms);
+  p.r = (N + rounds * sms - 1) / (rounds * sms);
+  if (MX && GATEUP) p.r = (p.r + 31) / 32 * 32;
+  if (p.r < unit) p.r = unit;
+  p.tiles = (N + p.r - 1) / p.r;
+  const bool one = p.tiles <= sms;  // one tile per CTA
+  const auto rows8 = [&](int s) { return (s * p.r + 7) / 8 * 8; };
+  p.s = 1;
+  const int most = GATEUP ? 64 : 128;  // operand rows of one weight
+  if (one && p.z)
+    while (2 * p.s <= (MX ? 4 : 8) && rows8(2 * p.s) <= most && 2 * p.s * T <= MAX_N && 2 * p.s <= p.KB) p.s *= 2;
+  p.w_rows = rows8(p.s);
+  p.merged = GATEUP && one && p.w_rows <= most;
+  p.staged = p.merged || p.s > 1;
+  p.KS = (p.KB + p.s - 1) / p.s;
+  p.mma_n = (p.s * T + 15) / 16 * 16;
+  p.cs = 1;
+  if (MX && p.merged)
+    while (2 * p.cs <= MAX_CLUSTER && 2 * p.cs * p.tiles <= sms && p.KS >= 8 * p.cs) p.cs *= 2;
+  p.stage_bytes = (GATEUP ? 2 : 1) * p.w_rows * ROW_BYTES + p.mma_n * ROW_BYTES;
+  p.sf_w1 = p.merged ? 0 : 512;
+  p.sf_x = GATEUP && !p.merged ? 1024 : 512;
+  p.sf_bytes = p.sf_x + (p.mma_n + 127) / 128 * 512;
+  const int sf_ring = MX ? SF_SLOTS * p.sf_bytes : 0;
+  const long long all = (long long)p.KS / p.cs * p.stage_bytes * ((p.tiles + sms - 1) / sms);
+  p.stages = ((GATEUP ? RING_GATEUP : RING_DOWN) - sf_ring) / p.stage_bytes;
+  if (p.stages < 4 || all > SHORT_BYTES) p.stages = (RING_ALONE - sf_ring) / p.stage_bytes;
+  if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+  p.stages -= p.stages % ISSUERS;
+  const int reach = (GATEUP && !p.merged ? p.w_rows * ROW_BYTES : 0) + OPERAND_BYTES;  // of the operands of a stage
+  p.ring_bytes = p.stages * p.stage_bytes + (reach > p.stage_bytes ? reach - p.stage_bytes : 0);
+  p.acc_cols = (GATEUP && !p.merged ? 2 : 1) * p.mma_n;
+  const int more = MX ? 2 * ISSUERS * SF_SLOT_COLS : p.s > 1 ? 16 : 0;  // 16: what a last read may pass them by
+  p.acc_bufs = one || 2 * ISSUERS * p.acc_cols + more > 512 ? 1 : 2;
+  const int cols = p.acc_bufs * ISSUERS * p.acc_cols + more;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < cols) p.tmem_cols *= 2;
+  p.status = moe_host::device_status_ptr();
+  return p;
+}
+
+// Tensor map of a row-major [rows, K] operand: boxes of 128 bytes x box rows x s blocks of K.
+template <bool MX>
+bool encode_map(CUtensorMap* m, const Params& p, const void* base, int rows, int box) {
+  const uint64_t eb = MX ? 1 : 2, step = MX ? 128 : 64;
+  return moe_host::encode_tmap_3d(m, MX ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
+                                  p.z ? step : (uint64_t)p.K, rows, p.z ? p.KB : 1, p.K * eb, ROW_BYTES, step, box,
+                                  p.s);
+}
+
+// The weights [K, N] of the down product that follows a gate/up launch: up to NEXT_BYTES of them beyond what its
+// ring takes are asked into L2 (about what memory delivers while the one kernel ends and the other begins).
+constexpr long long NEXT_BYTES = 48ll << 20;
+template <bool MX>
+bool plan_next(Params& p, const void* W_next) {
+  const Params d = plan<MX, false>(p.T, p.K, p.N);
+  if (!d.z) return true;  // ragged K: one small box per stage, not worth it
+  p.next_r = d.r;
+  p.next_s = d.s;
+  p.next_tiles = d.tiles;
+  p.next_from = d.stages;
+  const long long n = d.stages + NEXT_BYTES / ((long long)d.tiles * d.s * d.r * ROW_BYTES);
+  p.next_to = (int)(n < d.KS ? n : d.KS);
+  return encode_map<MX>(&p.tmNext, d, W_next, d.N, d.r);
+}
+
+// dep: the kernel before it in the stream is one of the same call's (the weights are not its results).
+template <bool MX, bool GATEUP>
+int launch(const Params& p, cudaStream_t st, bool dep) {
+  auto kern = gemm_kernel<MX, GATEUP>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_ALONE + OPERAND_BYTES + SMEM_FIXED) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg{};
+  const int sms = moe_host::num_sms();
+  cfg.gridDim = dim3(p.cs > 1 ? p.tiles * p.cs : p.tiles < sms ? p.tiles : sms);
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = p.ring_bytes + (MX ? SF_SLOTS * p.sf_bytes : 0) + SMEM_FIXED;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2] = {};
+  int n = 0;
+  if (dep) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (p.cs > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = p.cs;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+}  // namespace stream

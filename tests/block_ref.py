@@ -92,12 +92,12 @@ def ffn_bwd(dy, x, W_g, W_u, W_d):
 
 
 def check_sum(got, ref, sigma, rel, K):
-    """A bf16 result of a K-term sum whose terms carry independent errors of root mean square `rel` (relative), where
-    sigma = sqrt(sum of the terms' squares): its own rounding, eight standard deviations of the terms' errors (which
-    also covers the worst case of up to 64 terms: sqrt(K) sqrt(3) rel sigma for errors bounded by sqrt(3) rel needs
-    sqrt(3 K) <= 8 for K <= 21, and beyond it eight deviations of a sum of bounded errors are passed with
-    probability below 2 exp(-32 / 3)... per element of errors at their bound only), and fp32 sums: each of the K
-    additions is off by at most 2^-23 of a partial sum (the tensor core truncates), of the order of sigma."""
+    """A bf16 result of a K-term sum whose terms carry independent errors of root mean square `rel` (relative), with
+    sigma = sqrt(sum of the terms' squares). Allowed: its own rounding; eight standard deviations of the terms' errors
+    (an error is at most sqrt(3) rel of its term, so up to 21 terms this covers the worst case, sqrt(3 K) <= 8; with
+    more, a sum of bounded independent errors passes 8 deviations with a probability below 2 exp(-32 / 3), and only if
+    all its errors are at their bounds); and the fp32 additions, each off by at most 2^-23 (the tensor core truncates)
+    of a partial sum of the order of sigma."""
     got, ref, sigma = got.double().cpu(), ref.double().cpu(), sigma.double().cpu()
     assert got.shape == ref.shape
     tol = U * ref.abs() + (8 * rel + 2 * F32 * K) * sigma + 1e-30
