@@ -7,15 +7,21 @@
 // Everything past an edge of M, N or K is zero-filled by TMA on the way in and
 // predicated on the way out, so no operand is padded.
 //
+// Two forms (template CG):
+//   1  a CTA computes 128 x 256 (tcgen05 M128 N256 K16), four 48 KB stages;
+//   2  a pair of CTAs on neighbouring SMs computes 256 x 256 with
+//      cta_group::2: each holds its 128 rows of A and half of B's 256 rows, so
+//      a stage is 32 KB per SM, six fit, and every SM moves a third less
+//      through L2 and shared memory per product. Taken where rounding M up to
+//      256 costs little.
 // Roles (320 threads, one CTA per SM, persistent), as in the grouped GEMM of
-// gemm.cuh: warp 0 TMA producer (four stages of A 128 x 64 and B 256 x 64,
-// 128-byte swizzle), warp 1 MMA issuer (M128 N256 K16) and TMEM owner (two
-// 256-column accumulators), warps 2..9 epilogue (lane quadrant w % 4, column
-// half). Every wait is bounded (MOE_WAIT_NS).
+// gemm.cuh: warp 0 TMA producer, warp 1 MMA issuer (the pair's first CTA) and
+// TMEM owner (two 256-column accumulators), warps 2..9 epilogue (lane quadrant
+// w % 4, column half). Every wait is bounded (MOE_WAIT_NS).
 //
-// Work split. Whole tiles go round robin over the CTAs while they fill every
-// SM; the rest (all tiles, when there are fewer than SMs) is one line of
-// k-blocks that is cut into equal pieces, one per CTA. A piece that holds a
+// Work split. Whole tiles go round robin over the CTAs (pairs) while they fill
+// every SM; a rest that would leave many idle for long is one line of k-blocks
+// instead, cut into equal pieces, one per CTA (pair). A piece that holds a
 // whole tile is finished in place; the others leave fp32 partial accumulators
 // in the workspace (at most two per CTA), and fixup_kernel adds them in the
 // order of K and applies the epilogue, so results do not depend on timing.
@@ -27,18 +33,15 @@
 namespace dense {
 
 constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int kStages = 4;
-constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int A_BYTES = BM * BK * 2;
 constexpr int EPI_WARPS = 8;
 constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 2 * BN;
 constexpr int STG_ROW = 80;  // staging: 32 rows x (64 + 16) bytes per epilogue warp
 constexpr int STG_BYTES = EPI_WARPS * 32 * STG_ROW;
 constexpr int BAR_BYTES = 256;
-constexpr int SMEM_BYTES = 1024 + kStages * STAGE_BYTES + BAR_BYTES + STG_BYTES;
-static_assert(SMEM_BYTES <= 232448, "shared memory");
 constexpr int MAX_CTAS = 160;                            // CTAs of one launch (one per SM)
-constexpr size_t SLOT_FLOATS = (size_t)BM * BN;          // one partial accumulator
+constexpr size_t SLOT_FLOATS = (size_t)BM * BN;          // one CTA's partial accumulator
 constexpr size_t PART_BYTES = 2ull * MAX_CTAS * SLOT_FLOATS * sizeof(float);
 
 enum Op : int {
@@ -54,11 +57,12 @@ struct __align__(64) Params {
   int M, N;            // output rows and columns (per half when m_split)
   int KB;              // k-blocks of 64
   int kb_split;        // OP_DGRAD_X: k-blocks of the first half
+  int halves;          // OP_WGRAD: 2 for two stacked outputs of M rows each (A2, C2 the second), else 1
   int tiles_m, tiles_n;
-  int tm_split;        // OP_WGRAD: m-tiles of the first half (tiles_m when there is one)
+  int tm_split;        // m-tiles of one half
   int n_full;          // tiles done whole, round robin
   int sk_tiles;        // tiles n_full .. n_full + sk_tiles - 1, cut along K
-  int sk_per;          // k-blocks per CTA of those
+  int sk_per;          // k-blocks per CTA (pair) of those
   float* part;
   __nv_bfloat16* C;
   __nv_bfloat16* C2;
@@ -74,15 +78,16 @@ struct Seg {
   int slot;  // >= 0: partial accumulator to leave there
 };
 
-// The it-th piece of work of CTA b: first its cut of the k-block line, then whole tiles.
+// The pieces of work of CTA (pair) w of n: first its cut of the k-block line, then whole tiles.
 struct Walk {
-  int u, end, t, step;
-  MOE_DEV Walk(const Params& p) {
+  int w, u, end, t, step;
+  MOE_DEV Walk(const Params& p, int w_, int n) {
     const int units = p.sk_tiles * p.KB;
-    u = min((int)blockIdx.x * p.sk_per, units);
+    w = w_;
+    u = min(w * p.sk_per, units);
     end = min(u + p.sk_per, units);
-    t = blockIdx.x;
-    step = gridDim.x;
+    t = w;
+    step = n;
   }
   MOE_DEV Seg next(const Params& p) {
     Seg s;
@@ -91,7 +96,7 @@ struct Walk {
       s.kb0 = u - i * p.KB;
       s.nkb = min(p.KB - s.kb0, end - u);
       s.tile = p.n_full + i;
-      s.slot = s.nkb == p.KB ? -1 : 2 * (int)blockIdx.x + (s.kb0 > 0 ? 0 : 1);
+      s.slot = s.nkb == p.KB ? -1 : 2 * w + (s.kb0 > 0 ? 0 : 1);
       u += s.nkb;
       return s;
     }
@@ -104,28 +109,111 @@ struct Walk {
   }
 };
 
-template <int OP>
+template <int OP, int CG>
 struct Cfg {
   static constexpr bool A_MN = OP == OP_WGRAD;
   static constexpr bool B_MN = OP >= OP_DGRAD_ACT;
   static constexpr int N_STEP = OP == OP_GATEUP ? BN / 2 : BN;  // output columns per tile
+  static constexpr int B_ROWS = BN / CG;                        // of B, per CTA
+  static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK * 2;
+  static constexpr int kStages = CG == 2 ? 6 : 4;
+  static constexpr int SMEM_BYTES = 1024 + kStages * STAGE_BYTES + BAR_BYTES + STG_BYTES;
+  static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
 struct Origin {
-  int mt, m0, n0, rows, cols;  // m0, n0 within the (half) output; rows, cols: valid extent
-  bool second;                 // OP_WGRAD: the second half
+  int m0, n0, rows, cols;  // m0, n0 within the (half) output, m0 of this CTA; rows, cols: valid extent (may be <= 0)
+  bool second;             // OP_WGRAD: the second half
 };
-template <int OP>
-MOE_DEV Origin origin(const Params& p, int tile) {
+// rank: the CTA's place in its pair.
+template <int OP, int CG>
+MOE_DEV Origin origin(const Params& p, int tile, int rank) {
   Origin o;
-  o.mt = tile % p.tiles_m;  // m fastest: the CTAs of a wave share a few column panels of B
+  const int mt = tile % p.tiles_m;  // m fastest: the CTAs of a wave share a few column panels of B
   const int nt = tile / p.tiles_m;
-  o.second = OP == OP_WGRAD && o.mt >= p.tm_split;
-  o.m0 = (o.mt - (o.second ? p.tm_split : 0)) * BM;
-  o.n0 = nt * Cfg<OP>::N_STEP;
+  o.second = OP == OP_WGRAD && mt >= p.tm_split;
+  o.m0 = (mt - (o.second ? p.tm_split : 0)) * BM * CG + rank * BM;
+  o.n0 = nt * Cfg<OP, CG>::N_STEP;
   o.rows = min(BM, p.M - o.m0);
-  o.cols = min(Cfg<OP>::N_STEP, p.N - o.n0);
+  o.cols = min(Cfg<OP, CG>::N_STEP, p.N - o.n0);
   return o;
+}
+
+// ---------------------------------------------------------------- CTA pairs
+
+// Shared-memory address of the pair's CTA `rank`.
+MOE_DEV uint32_t pair_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+MOE_DEV void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <int CG>
+MOE_DEV void load_tile(void* dst, const CUtensorMap* m, int x, int y, uint64_t* bar) {
+  if constexpr (CG == 1) {
+    tma_load_2d(dst, m, x, y, bar);
+  } else {
+    // the bytes are counted on the first CTA's barrier
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(pair_addr(smem_u32(bar), 0))
+        : "memory");
+  }
+}
+template <int CG>
+MOE_DEV void mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 1)
+    mma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on the barrier (of both CTAs of a pair) once every MMA issued so far is done.
+template <int CG>
+MOE_DEV void commit(uint64_t* bar) {
+  if constexpr (CG == 1) {
+    mma_commit(bar);
+  } else {
+#pragma unroll
+    for (uint32_t r = 0; r < 2; ++r)
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                       pair_addr(smem_u32(bar), r))
+                   : "memory");
+  }
+}
+// Arrives on the first CTA's barrier.
+template <int CG>
+MOE_DEV void arrive_first(uint64_t* bar) {
+  if constexpr (CG == 1)
+    mbar_arrive(bar);
+  else
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(pair_addr(smem_u32(bar), 0))
+                 : "memory");
+}
+template <int CG>
+MOE_DEV void alloc_tmem(uint32_t* slot) {
+  if constexpr (CG == 1) {
+    tmem_alloc(slot, TMEM_COLS);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+MOE_DEV void free_tmem(uint32_t taddr) {
+  if constexpr (CG == 1)
+    tmem_dealloc(taddr, TMEM_COLS);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(TMEM_COLS) : "memory");
 }
 
 // 32 bf16 of each of the warp's 32 rows (16 words per lane, lane = row) to dst (row-contiguous through the
@@ -180,12 +268,13 @@ MOE_DEV void pack32(const float (&v)[32], uint32_t (&w)[16]) {
 MOE_DEV float word_lo(uint32_t w) { return __uint_as_float(w << 16); }
 MOE_DEV float word_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-template <int OP>
+template <int OP, int CG>
 __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<OP>;
+  using C = Cfg<OP, CG>;
+  constexpr int kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* stg_area = smem + kStages * STAGE_BYTES;
+  uint8_t* stg_area = smem + kStages * C::STAGE_BYTES;
   uint64_t* full = reinterpret_cast<uint64_t*>(stg_area + STG_BYTES);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
@@ -195,6 +284,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? (int)blockIdx.x & 1 : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -202,17 +292,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], EPI_WARPS);
+      mbar_init(&tempty[i], CG * EPI_WARPS);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
-    tmem_relinquish();
+  if (threadIdx.x == 64) {
+    tma_prefetch_desc(&p.tmA);
+    tma_prefetch_desc(&p.tmB0);
   }
+  if (warp == 1) alloc_tmem<CG>(tmem_slot);
   __syncthreads();
+  if (CG == 2) pair_sync();  // both CTAs' barriers exist before either signals the other
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   // launched over the tail of the kernel before it: its results are visible from here on
@@ -220,42 +312,51 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
   griddep_launch_dependents();
 
   bool aborted = false;
-  Walk walk(p);
+  Walk walk(p, (int)blockIdx.x / CG, (int)gridDim.x / CG);
   if (warp == 0) {
-    // ======================= TMA producer
+    // ======================= TMA producer: this CTA's rows of A and B
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, issued_mask = 0, issued_par = 0;
       for (Seg s = walk.next(p); s.tile >= 0 && !aborted; s = walk.next(p)) {
-        const Origin o = origin<OP>(p, s.tile);
+        const Origin o = origin<OP, CG>(p, s.tile, rank);
+        const int b0 = o.n0 + (OP == OP_GATEUP ? 0 : rank * C::B_ROWS);
         for (int kb = s.kb0; kb < s.kb0 + s.nkb; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) {
             aborted = true;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * C::STAGE_BYTES);
           issued_mask |= 1u << stage;
           issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-          uint8_t* sA = smem + stage * STAGE_BYTES;
+          uint8_t* sA = smem + stage * C::STAGE_BYTES;
           uint8_t* sB = sA + A_BYTES;
+          uint64_t* bar = &full[stage];
           const bool hi = OP == OP_DGRAD_X && kb >= p.kb_split;  // the up half of K
           const int kc = (kb - (hi ? p.kb_split : 0)) * BK;
           const CUtensorMap* mA = (hi || o.second) ? &p.tmA2 : &p.tmA;
           if constexpr (!C::A_MN) {
-            tma_load_2d(sA, mA, kc, o.m0, &full[stage]);
+            load_tile<CG>(sA, mA, kc, o.m0, bar);
           } else {
-            tma_load_2d(sA, mA, o.m0, kc, &full[stage]);
-            tma_load_2d(sA + 64 * BK * 2, mA, o.m0 + 64, kc, &full[stage]);
+            load_tile<CG>(sA, mA, o.m0, kc, bar);
+            load_tile<CG>(sA + 64 * BK * 2, mA, o.m0 + 64, kc, bar);
           }
-          if constexpr (!C::B_MN) {
-            tma_load_2d(sB, &p.tmB0, kc, o.n0, &full[stage]);
-            if (OP == OP_GATEUP) tma_load_2d(sB + 128 * BK * 2, &p.tmB1, kc, o.n0, &full[stage]);
-            else tma_load_2d(sB + 128 * BK * 2, &p.tmB0, kc, o.n0 + 128, &full[stage]);
+          if constexpr (OP == OP_GATEUP) {
+            // columns 0..127 of the accumulator are gate, 128..255 up
+            if constexpr (CG == 2) {
+              load_tile<CG>(sB, rank ? &p.tmB1 : &p.tmB0, kc, b0, bar);
+            } else {
+              load_tile<CG>(sB, &p.tmB0, kc, b0, bar);
+              load_tile<CG>(sB + 128 * BK * 2, &p.tmB1, kc, b0, bar);
+            }
+          } else if constexpr (!C::B_MN) {
+#pragma unroll
+            for (int j = 0; j < C::B_ROWS / 128; ++j)
+              load_tile<CG>(sB + j * 128 * BK * 2, &p.tmB0, kc, b0 + 128 * j, bar);
           } else {
             const CUtensorMap* mB = hi ? &p.tmB1 : &p.tmB0;
 #pragma unroll
-            for (int j = 0; j < BN / 64; ++j)
-              tma_load_2d(sB + j * 64 * BK * 2, mB, o.n0 + 64 * j, kc, &full[stage]);
+            for (int j = 0; j < C::B_ROWS / 64; ++j) load_tile<CG>(sB + j * 64 * BK * 2, mB, b0 + 64 * j, kc, bar);
           }
           if (++stage == kStages) {
             stage = 0;
@@ -263,22 +364,36 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
           }
         }
       }
+      if (CG == 2) {
+        // no commit of the first CTA may arrive here after this CTA has left: wait until every stage is released
+        for (int i = 0; i < kStages && !aborted; ++i) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) aborted = true;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
       if (*abort_flag) {
-        // every TMA this thread issued must land before the CTA exits
+        // every TMA this thread issued must land before the CTA exits (a pair's second CTA cannot see its own land:
+        // it gives them a time)
+        const uint64_t t1 = globaltimer_ns();
         for (int i = 0; i < kStages; ++i)
           if (issued_mask & (1u << i)) {
             const uint32_t par = (issued_par >> i) & 1u;
             const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(&full[i], par) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
+            while (rank == 0 && !mbar_try_wait(&full[i], par) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
             }
           }
+        while (CG == 2 && globaltimer_ns() - t1 < 1000000ull) {
+        }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ======================= MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t IDESC = idesc_bf16(BM, BN, C::A_MN ? 1 : 0, C::B_MN ? 1 : 0);
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t IDESC = idesc_bf16(CG * BM, BN, C::A_MN ? 1 : 0, C::B_MN ? 1 : 0);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       for (Seg s = walk.next(p); s.tile >= 0 && !aborted; s = walk.next(p)) {
@@ -294,23 +409,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + stage * STAGE_BYTES), b0 = a0 + A_BYTES;
+          const uint32_t a0 = smem_u32(smem + stage * C::STAGE_BYTES), b0 = a0 + A_BYTES;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
             const uint64_t ad = C::A_MN ? smem_desc_sw128(a0 + kk * 2048, 64 * BK * 2, 1024)
                                         : smem_desc_sw128(a0 + kk * 32, 16, 1024);
             const uint64_t bd = C::B_MN ? smem_desc_sw128(b0 + kk * 2048, 64 * BK * 2, 1024)
                                         : smem_desc_sw128(b0 + kk * 32, 16, 1024);
-            mma_bf16(d_tmem, ad, bd, IDESC, (kb | kk) != 0 ? 1u : 0u);
+            mma<CG>(d_tmem, ad, bd, IDESC, (kb | kk) != 0 ? 1u : 0u);
           }
-          mma_commit(&empty[stage]);
+          commit<CG>(&empty[stage]);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (aborted) break;
-        mma_commit(&tfull[acc]);
+        commit<CG>(&tfull[acc]);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1;
@@ -318,7 +433,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
       }
       if (*abort_flag) {
         // wait for every MMA already issued before TMEM is released
-        mma_commit(drain);
+        commit<CG>(drain);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
         }
@@ -337,13 +452,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
         break;
       }
       tc_fence_after();
-      const Origin o = origin<OP>(p, s.tile);
+      const Origin o = origin<OP, CG>(p, s.tile, rank);
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN;
       const int rows = o.rows - 32 * q;  // of this warp's 32 (may be <= 0)
       const long long row0 = (long long)o.m0 + 32 * q;
       if (s.slot >= 0) {
         // fp32 partial, column-major: a warp store writes one column's 32 rows
-        float* dst = p.part + (size_t)s.slot * SLOT_FLOATS + 32 * q + lane;
+        float* dst = p.part + (size_t)(s.slot * CG + rank) * SLOT_FLOATS + 32 * q + lane;
         const bool ok = lane < rows;
 #pragma unroll 1
         for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
@@ -418,7 +533,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[acc]);
+      if (lane == 0) arrive_first<CG>(&tempty[acc]);
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1;
@@ -426,32 +541,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
     }
   }
   __syncthreads();
+  if (CG == 2) pair_sync();  // everything the pair sends each other has arrived
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    free_tmem<CG>(tmem_base);
   }
 }
 
 // Adds the partial accumulators of every tile that was cut (in the order of K) and applies the epilogue.
 // Thread: one row and 8 output columns; grid.x: tiles, grid.y: column groups of CTA_COLS.
 constexpr int FIX_THREADS = 256;
-template <int OP>
+template <int OP, int CG>
 __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constant__ Params p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int i = blockIdx.x;
+  const int i = blockIdx.x / CG, rank = CG == 2 ? (int)blockIdx.x & 1 : 0;
   const int b0 = (int)((long long)i * p.KB / p.sk_per), b1 = (int)(((long long)(i + 1) * p.KB - 1) / p.sk_per);
-  if (b0 == b1) return;  // one CTA held the whole tile and finished it
-  const Origin o = origin<OP>(p, p.n_full + i);
+  if (b0 == b1) return;  // one CTA (pair) held the whole tile and finished it
+  const Origin o = origin<OP, CG>(p, p.n_full + i, rank);
+  if (o.rows <= 0) return;
   const int groups = (o.cols + 7) / 8;
   for (int e = blockIdx.y * FIX_THREADS + threadIdx.x; e < groups * o.rows; e += gridDim.y * FIX_THREADS) {
     const int r = e % o.rows, c = 8 * (e / o.rows);
     float v[8], u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
+#pragma unroll 4
     for (int b = b0; b <= b1; ++b) {
       const int slot = 2 * b + (b * p.sk_per > i * p.KB ? 0 : 1);
-      const float* src = p.part + (size_t)slot * SLOT_FLOATS + (size_t)c * BM + r;
+      const float* src = p.part + (size_t)(slot * CG + rank) * SLOT_FLOATS + (size_t)c * BM + r;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[j] += src[j * BM];
@@ -490,17 +608,26 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
 
 // Launch with programmatic dependence on the kernel before it in the stream (every kernel here waits for it).
 template <class K>
-int launch_dep(K kern, dim3 grid, int threads, size_t smem, cudaStream_t st, const Params& p, bool dep) {
+int launch_dep(K kern, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, const Params& p, bool dep) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = dep ? 1 : 0;
+  cudaLaunchAttribute at[2] = {};
+  int n = 0;
+  if (dep) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = cluster;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
   if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
@@ -508,25 +635,75 @@ int launch_dep(K kern, dim3 grid, int threads, size_t smem, cudaStream_t st, con
   return MOE_OK;
 }
 
+// Pairs of CTAs that can be resident at once on the current device.
+template <int OP>
+int max_pairs() {
+  static int cached[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  if (!cached[dev]) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * (MAX_CTAS / 2));
+    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.dynamicSmemBytes = Cfg<OP, 2>::SMEM_BYTES;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, gemm_kernel<OP, 2>, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      n = 0;
+    }
+    cached[dev] = n > 0 ? n : -1;
+  }
+  return cached[dev] > 0 ? cached[dev] : 0;
+}
+
+template <int OP, int CG>
+int launch_cg(Params& p, int workers, cudaStream_t st, bool dep) {
+  using C = Cfg<OP, CG>;
+  const int per = (p.M + BM * CG - 1) / (BM * CG);
+  p.tiles_m = p.halves * per;
+  p.tm_split = per;
+  p.tiles_n = (p.N + C::N_STEP - 1) / C::N_STEP;
+  const long long total = (long long)p.tiles_m * p.tiles_n;
+  const int rest = (int)(total % workers);
+  // Cutting the rest along K saves (1 - rest / workers) of a tile's time, about 0.27 us per k-block, and costs
+  // about 8 us (partial sums out and in again, one more kernel).
+  const bool cut = rest && (long long)(workers - rest) * p.KB > 30ll * workers;
+  p.n_full = (int)(cut ? total - rest : total);
+  p.sk_tiles = cut ? rest : 0;
+  p.sk_per = cut ? (rest * p.KB + workers - 1) / workers : 0;
+  auto kern = gemm_kernel<OP, CG>;
+  int n = workers;
+  if (!cut && total < n) n = (int)total;
+  int rc = launch_dep(kern, dim3(n * CG), NUM_THREADS, C::SMEM_BYTES, CG, st, p, dep);
+  if (rc || !cut) return rc;
+  return launch_dep(fixup_kernel<OP, CG>, dim3(rest * CG, OP == OP_GATEUP ? 8 : 16), FIX_THREADS, 0, 1, st, p, true);
+}
+
 // dep: the kernel before it in the stream is one of the same call's.
 template <int OP>
 int launch(Params& p, cudaStream_t st, bool dep) {
-  p.tiles_n = (p.N + Cfg<OP>::N_STEP - 1) / Cfg<OP>::N_STEP;
-  const long long total = (long long)p.tiles_m * p.tiles_n;
-  int sms = moe_host::num_sms();
-  if (sms > MAX_CTAS) sms = MAX_CTAS;
-  const int rest = (int)(total % sms);
-  p.n_full = (int)(total - rest);
-  p.sk_tiles = rest;
-  p.sk_per = rest ? (rest * p.KB + sms - 1) / sms : 0;
-  auto kern = gemm_kernel<OP>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess) {
+  if (cudaFuncSetAttribute(gemm_kernel<OP, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Cfg<OP, 1>::SMEM_BYTES) != cudaSuccess ||
+      cudaFuncSetAttribute(gemm_kernel<OP, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Cfg<OP, 2>::SMEM_BYTES) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }
-  int rc = launch_dep(kern, dim3(sms), NUM_THREADS, SMEM_BYTES, st, p, dep);
-  if (rc || !rest) return rc;
-  return launch_dep(fixup_kernel<OP>, dim3(rest, OP == OP_GATEUP ? 8 : 16), FIX_THREADS, 0, st, p, true);
+  int sms = moe_host::num_sms();
+  if (sms > MAX_CTAS) sms = MAX_CTAS;
+  const int m1 = (p.M + BM - 1) / BM, m2 = (p.M + 2 * BM - 1) / (2 * BM) * 2;
+  const int pairs = max_pairs<OP>();
+  if (m2 * 16 <= m1 * 17 && 2 * pairs >= sms - 2) return launch_cg<OP, 2>(p, pairs < sms / 2 ? pairs : sms / 2, st, dep);
+  return launch_cg<OP, 1>(p, sms, st, dep);
 }
 
 }  // namespace dense

@@ -108,7 +108,7 @@ static Params base_params(int M, int N, int KB, float* part, void* C, long long 
   p.M = M;
   p.N = N;
   p.KB = KB;
-  p.tiles_m = p.tm_split = cdiv(M, dense::BM);
+  p.halves = 1;
   p.part = part;
   p.C = static_cast<__nv_bfloat16*>(C);
   p.ldc = ldc;
@@ -157,7 +157,7 @@ static int wgrad(int T, int M, int N, const void* dO, const void* dO2, long long
   if (!tmap(&p.tmA, dO, M, T, ld_dO, 64) || !tmap(&p.tmB0, act, N, T, N, 64)) return MOE_ERR_CUDA;
   if (dO2) {
     if (!tmap(&p.tmA2, dO2, M, T, ld_dO, 64)) return MOE_ERR_CUDA;
-    p.tiles_m = 2 * p.tm_split;
+    p.halves = 2;
     p.C2 = static_cast<__nv_bfloat16*>(dW2);
   }
   return dense::launch<dense::OP_WGRAD>(p, st, dep);
