@@ -57,6 +57,7 @@ struct __align__(64) Params {
   int M, N;            // output rows and columns (per half when m_split)
   int KB;              // k-blocks of 64
   int kb_split;        // OP_DGRAD_X: k-blocks of the first half
+  int ragged;          // an operand's rows do not start on 128 bytes
   int halves;          // OP_WGRAD: 2 for two stacked outputs of M rows each (A2, C2 the second), else 1
   int tiles_m, tiles_n;
   int tm_split;        // m-tiles of one half
@@ -674,9 +675,10 @@ int launch_cg(Params& p, int workers, cudaStream_t st, bool dep) {
   p.tiles_n = (p.N + C::N_STEP - 1) / C::N_STEP;
   const long long total = (long long)p.tiles_m * p.tiles_n;
   const int rest = (int)(total % workers);
-  // Cutting the rest along K saves (1 - rest / workers) of a tile's time, about 0.27 us per k-block, and costs
-  // about 8 us (partial sums out and in again, one more kernel).
-  const bool cut = rest && (long long)(workers - rest) * p.KB > 30ll * workers;
+  // Cutting the rest along K saves (1 - rest / workers) of a tile's time, about 0.27 us per k-block (0.7 where rows
+  // do not start on 128 bytes: every row of a box is then on two lines), and costs about 6 us (partial sums out and
+  // in again, one more kernel).
+  const bool cut = rest && (long long)(workers - rest) * p.KB > (p.ragged ? 9ll : 22ll) * workers;
   p.n_full = (int)(cut ? total - rest : total);
   p.sk_tiles = cut ? rest : 0;
   p.sk_per = cut ? (rest * p.KB + workers - 1) / workers : 0;

@@ -103,8 +103,10 @@ static bool tmap(CUtensorMap* m, const void* base, long long inner, long long ou
 }
 static int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-static Params base_params(int M, int N, int KB, float* part, void* C, long long ldc) {
+// H, F: the block's sizes (every operand's row length).
+static Params base_params(int H, int F, int M, int N, int KB, float* part, void* C, long long ldc) {
   Params p{};
+  p.ragged = H % 64 != 0 || F % 64 != 0;
   p.M = M;
   p.N = N;
   p.KB = KB;
@@ -118,7 +120,7 @@ static Params base_params(int M, int N, int KB, float* part, void* C, long long 
 
 static int gateup(int T, int H, int F, const void* x, const void* Wg, const void* Wu, void* a, void* save, float* part,
                   cudaStream_t st, bool dep) {
-  Params p = base_params(T, F, cdiv(H, dense::BK), part, a, F);
+  Params p = base_params(H, F, T, F, cdiv(H, dense::BK), part, a, F);
   if (!tmap(&p.tmA, x, H, T, H, 128) || !tmap(&p.tmB0, Wg, H, F, H, 128) || !tmap(&p.tmB1, Wu, H, F, H, 128))
     return MOE_ERR_CUDA;
   p.save = static_cast<__nv_bfloat16*>(save);
@@ -126,14 +128,14 @@ static int gateup(int T, int H, int F, const void* x, const void* Wg, const void
 }
 
 static int down(int T, int H, int F, const void* a, const void* Wd, void* y, float* part, cudaStream_t st, bool dep) {
-  Params p = base_params(T, H, cdiv(F, dense::BK), part, y, H);
+  Params p = base_params(H, F, T, H, cdiv(F, dense::BK), part, y, H);
   if (!tmap(&p.tmA, a, F, T, F, 128) || !tmap(&p.tmB0, Wd, F, H, F, 128)) return MOE_ERR_CUDA;
   return dense::launch<dense::OP_DOWN>(p, st, dep);
 }
 
 static int dgrad_act(int T, int H, int F, const void* dY, const void* Wd, const void* gateup, void* dgu, float* part,
                      cudaStream_t st, bool dep) {
-  Params p = base_params(T, F, cdiv(H, dense::BK), part, dgu, 2LL * F);
+  Params p = base_params(H, F, T, F, cdiv(H, dense::BK), part, dgu, 2LL * F);
   if (!tmap(&p.tmA, dY, H, T, H, 128) || !tmap(&p.tmB0, Wd, F, H, F, 64)) return MOE_ERR_CUDA;
   p.gateup = static_cast<const __nv_bfloat16*>(gateup);
   return dense::launch<dense::OP_DGRAD_ACT>(p, st, dep);
@@ -142,7 +144,7 @@ static int dgrad_act(int T, int H, int F, const void* dY, const void* Wd, const 
 static int dgrad_x(int T, int H, int F, const __nv_bfloat16* dgu, const void* Wg, const void* Wu, void* dX,
                    float* part, cudaStream_t st, bool dep) {
   const int kb = cdiv(F, dense::BK);
-  Params p = base_params(T, H, 2 * kb, part, dX, H);
+  Params p = base_params(H, F, T, H, 2 * kb, part, dX, H);
   p.kb_split = kb;
   if (!tmap(&p.tmA, dgu, F, T, 2LL * F, 128) || !tmap(&p.tmA2, dgu + F, F, T, 2LL * F, 128) ||
       !tmap(&p.tmB0, Wg, H, F, H, 64) || !tmap(&p.tmB1, Wu, H, F, H, 64))
@@ -153,7 +155,7 @@ static int dgrad_x(int T, int H, int F, const __nv_bfloat16* dgu, const void* Wg
 // dW [M, N] = sum_t dO[t, :M]^T act[t, :N]; with dO2, a second [M, N] from it into dW2 in the same launch.
 static int wgrad(int T, int M, int N, const void* dO, const void* dO2, long long ld_dO, const void* act, void* dW,
                  void* dW2, float* part, cudaStream_t st, bool dep) {
-  Params p = base_params(M, N, cdiv(T, dense::BK), part, dW, N);
+  Params p = base_params(M, N, M, N, cdiv(T, dense::BK), part, dW, N);
   if (!tmap(&p.tmA, dO, M, T, ld_dO, 64) || !tmap(&p.tmB0, act, N, T, N, 64)) return MOE_ERR_CUDA;
   if (dO2) {
     if (!tmap(&p.tmA2, dO2, M, T, ld_dO, 64)) return MOE_ERR_CUDA;
@@ -170,8 +172,9 @@ static int stream_gemm(int T, int N, int K, const void* W0, const void* W1, cons
                        bool dep, const void* W_next = nullptr) {
   stream::Params p = stream::plan<MX, GATEUP>(T, N, K);
   if (GATEUP && !stream::plan_next<MX>(p, W_next)) return MOE_ERR_CUDA;
-  if (!stream::encode_map<MX>(&p.tmW0, p, W0, N, p.r) || (GATEUP && !stream::encode_map<MX>(&p.tmW1, p, W1, N, p.r)) ||
-      !stream::encode_map<MX>(&p.tmX, p, x, T, T))
+  if (!stream::encode_maps<MX>(&p.tmW0, &p.tmW0t, p, W0, N, p.r) ||
+      (GATEUP && !stream::encode_maps<MX>(&p.tmW1, &p.tmW1t, p, W1, N, p.r)) ||
+      !stream::encode_maps<MX>(&p.tmX, &p.tmXt, p, x, T, T))
     return MOE_ERR_CUDA;
   p.sf0 = sf0;
   p.sf1 = sf1;

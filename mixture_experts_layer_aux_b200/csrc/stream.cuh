@@ -34,8 +34,8 @@
 // the one ends and the other begins.
 //
 // Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer and TMEM owner
-// (MXFP8: warp 3 a second issuer; the rings then have an even number of stages,
-// so that a stage has one issuer, who sees each of its phases), warp 2 loader of the MXFP8 scales (natural [rows, K/32] layout -> the chunk
+// (where one is too slow, warp 3 is a second issuer; the rings then have an even
+// number of stages, so that a stage has one issuer, who sees all its phases), warp 2 loader of the MXFP8 scales (natural [rows, K/32] layout -> the chunk
 // order of the tensor-memory copies, see gemm_mx.cuh), warps 4..11 epilogue
 // (TMEM lane quadrant w % 4, every other 16 tokens). Every wait is bounded
 // (MOE_WAIT_NS).
@@ -59,14 +59,18 @@ constexpr int MAX_STAGES = 16;
 constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
 constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 // MMA issuers, each with accumulators of its own and every other stage: one thread's instructions (some 35 ns an MMA,
-// 60 a copy of scales or a commit) keep up with memory at 16 KB of bf16 per stage, not at MXFP8 with its scales (8
-// tokens, H = 7168, F = 2048: 28.7 us with one, 26.8 with two; bf16 is 2 us faster with one and an odd stage more).
-constexpr int issuers(bool mx) { return mx ? 2 : 1; }
+// 60 a copy of scales or a commit) keep up with memory at the two large operands of bf16 gate/up, not at 14 KB of
+// down weights per stage, or at MXFP8 with its scales (8 tokens, H = 7168, F = 2048: 28.7 us with one, 26.8 with
+// two).
+constexpr int issuers(bool mx, bool gateup) { return mx || !gateup ? 2 : 1; }
+// Kernels whose tiles may be shared by a cluster.
+constexpr bool clusters(bool mx, bool gateup) { return mx || !gateup; }
 constexpr int ROW_BYTES = 128;            // K bytes of a stage row (64 bf16 or 128 e4m3)
 constexpr int OPERAND_BYTES = 128 * ROW_BYTES;  // what an MMA reads of its weight operand, filled or not
 constexpr int MAX_N = 224;                // s T at most (two issuers' accumulators and the scales in 512 TMEM columns)
 constexpr int SF_SLOTS = 16;              // MXFP8: stages of scales in shared memory, on a ring of their own
 constexpr int SF_SLOT_COLS = 16;          // scale columns of a stage in TMEM (W0, W1: 128 rows; x: 256 rows)
+constexpr int MAX_PARTS = 9;              // K blocks of a stage, at most 8 (4 with MXFP8), and the tail
 constexpr int MAX_CLUSTER = 4;            // CTAs that share a tile, each taking a part of K
 constexpr int BAR_BYTES = 1024;
 // Bytes of the ring. A CTA with little to stream (up to SHORT_BYTES in all) leaves room for one of the other kernel
@@ -79,6 +83,7 @@ constexpr int SMEM_FIXED = 1024 + BAR_BYTES;
 
 struct __align__(64) Params {
   CUtensorMap tmW0, tmW1, tmX;
+  CUtensorMap tmW0t, tmW1t, tmXt;   // the part of K past its last whole block (tail != 0): 2-D maps
   CUtensorMap tmNext;               // gate/up: the down kernel's W0, its rows per tile, blocks per stage, tiles, and
   int next_r, next_s, next_tiles;   // the stages to bring into L2 (from, to)
   int next_from, next_to;
@@ -91,19 +96,23 @@ struct __align__(64) Params {
   int KB, KS;                       // K blocks (128 bytes), stages of s blocks
   int w_rows;                       // s r rounded up to 8: operand rows of one weight
   int mma_n;                        // s T rounded up to 16
-  int z;                            // tensor maps are cut along K (K a whole number of blocks; else s = 1)
+  int z;                            // tensor maps are cut along K; else s = 1
+  int tail;                         // K % 64 elements follow the whole blocks (bf16, one tile per CTA)
+  int r8, tail_n;                   // r rounded up to 8, T to 16: operand rows of the tail
+  int tail_bytes;                   // its place in shared memory, before the ring
   int tiles;
   int stages, stage_bytes;
   int ring_bytes;                   // the stages, and what the last one's operands read past it
   int sf_w1, sf_x, sf_bytes;        // MXFP8: offsets of W1's and x's chunks in a slot of scales, and its size
   int cs;                           // CTAs per tile (a cluster, each with a part of K), MXFP8 gate/up
   int acc_cols, acc_bufs, tmem_cols;  // TMEM: columns of one accumulator set, sets, allocation
+  int early;                        // launched over the tail of the kernel that makes x
   int merged;                       // gate/up: both weights in one operand
   int staged;                       // the epilogue goes through shared memory (s > 1, merged or cs > 1)
   int* status;
 };
 
-static_assert(SF_SLOTS % issuers(true) == 0, "a slot of scales has one issuer");
+static_assert(SF_SLOTS % 2 == 0, "a slot of scales has one issuer");
 
 // Instruction descriptors: bf16 (common.cuh) and MXFP8 (gemm_mx.cuh) with a run-time N.
 template <bool MX>
@@ -142,11 +151,14 @@ MOE_DEV void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
 MOE_DEV void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The same shared-memory address in CTA `rank` of the cluster, as a generic pointer.
-MOE_DEV const void* cluster_ptr(const void* p, uint32_t rank) {
-  uint64_t r;
-  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
-  return reinterpret_cast<const void*>(r);
+// The same shared-memory address in CTA `rank` of the cluster, and a store there.
+MOE_DEV uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+MOE_DEV void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // 4-byte asynchronous copy global -> shared; bytes 0: the destination is zeroed, nothing is read.
@@ -172,9 +184,10 @@ MOE_DEV uint8_t quant_lane(float a, uint8_t& sb) {
 
 template <bool MX, bool GATEUP>
 __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_constant__ Params p) {
-  constexpr int ISSUERS = issuers(MX);
+  constexpr int ISSUERS = issuers(MX, GATEUP);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* tail = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = tail + p.tail_bytes;
   uint8_t* sf_ring = ring + p.ring_bytes;
   uint8_t* bar_area = sf_ring + (MX ? SF_SLOTS * p.sf_bytes : 0);
   uint64_t* full = reinterpret_cast<uint64_t*>(bar_area);
@@ -183,15 +196,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
   uint64_t* sempty = sfull + SF_SLOTS;
   uint64_t* tfull = sempty + SF_SLOTS;
   uint64_t* tempty = tfull + 2;
-  uint64_t* staged = tempty + 2;
-  uint64_t* drain = staged + 1;
+  uint64_t* tail_full = tempty + 2;
+  uint64_t* drain = tail_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + ISSUERS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w_bytes = p.w_rows * ROW_BYTES;
   const int x_off = (GATEUP ? 2 : 1) * w_bytes;
-  // MXFP8 gate/up: cs consecutive CTAs (a cluster) share a tile; this one takes the stages [ks0, ks1) of K
-  constexpr bool CLUSTER = MX && GATEUP;
+  // cs consecutive CTAs (a cluster) share a tile; this one takes the stages [ks0, ks1) of K, the first the tail too
+  constexpr bool CLUSTER = clusters(MX, GATEUP);
   const int rank = CLUSTER ? (int)blockIdx.x % p.cs : 0;
   const int tile0 = CLUSTER ? (int)blockIdx.x / p.cs : (int)blockIdx.x;
   const int tile_step = CLUSTER ? (int)gridDim.x / p.cs : (int)gridDim.x;
@@ -210,7 +223,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
       mbar_init(&tfull[i], ISSUERS);
       mbar_init(&tempty[i], EPI_WARPS);
     }
-    mbar_init(staged, EPI_WARPS);
+    mbar_init(tail_full, 1);
     for (int i = 0; i < ISSUERS; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -229,42 +242,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
   const uint32_t tmem_base = *tmem_slot;
   griddep_launch_dependents();
 
-  // Staged epilogue, from shared memory on: adds the parts of every element, in the order of K, and writes it. A
-  // warp takes 32 columns of one token; the CTAs of a cluster divide the tokens among themselves.
-  const auto finish = [&](int t) {
-    const int n0 = t * p.r, rows = min(p.r, p.N - n0), cg = (p.r + 31) / 32;
-    const int first = (warp - EPI_WARP0) * (CLUSTER ? p.cs : 1) + rank, step = EPI_WARPS * (CLUSTER ? p.cs : 1);
-    for (int e = first; e < p.T * cg; e += step) {
-      const int tok = e / cg, f = 32 * (e - tok * cg) + lane;
-      const bool ok = f < rows;
-      float g = 0.f, u = 0.f;
-      if (ok)
-        for (int k = 0; k < (CLUSTER ? p.cs : 1); ++k) {
-          const float* st = reinterpret_cast<const float*>(CLUSTER && p.cs > 1 ? cluster_ptr(ring, k) : ring);
-          for (int c = 0; c < p.s; ++c) {
-            g += st[(c * p.T + tok) * p.r + f];
-            if (GATEUP) u += st[((p.s + c) * p.T + tok) * p.r + f];
-          }
-        }
-      const float a = GATEUP ? swiglu::act(g, u) : g;
-      const long long o = (long long)tok * p.N + n0 + f;
-      if (MX && GATEUP) {
-        uint8_t sb;
-        const uint8_t code = quant_lane(a, sb);
-        if (ok) {
-          static_cast<uint8_t*>(p.out)[o] = code;
-          if (lane == 0) p.out_sf[o >> 5] = sb;
-        }
-      } else if (ok) {
-        static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a);
-        if (GATEUP && p.save) {
-          __nv_bfloat16* sv = p.save + (long long)tok * 2 * p.N + n0 + f;
-          sv[0] = __float2bfloat16_rn(g);
-          sv[p.N] = __float2bfloat16_rn(u);
-        }
-      }
-    }
-  };
+  const bool with_tail = !MX && p.tail && rank == 0;
 
   bool aborted = false;
   if (warp == 0) {
@@ -285,13 +263,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
         if (GATEUP) load(&p.tmW1, t * p.r, ks, b + w_bytes, &full[st]);
       };
       // the first weights, before the wait for the kernel that makes x
-      const int ahead = min(p.stages, ks1 - ks0);
+      // (where there is none, a stage's tokens go out with its weights: behind the whole ring's they would be late)
+      const int ahead = p.early ? min(p.stages, ks1 - ks0) : 0;
       for (int st = 0; st < ahead; ++st) {
         mbar_arrive_expect_tx(&full[st], tx);
         issued_mask |= 1u << st;
         load_w(tile0, ks0 + st, st);
       }
+      if (with_tail) {
+        mbar_arrive_expect_tx(tail_full, (uint32_t)(((GATEUP ? 2 : 1) * p.r + p.T) * ROW_BYTES));
+        tma_load_2d(tail, &p.tmW0t, p.KB * kstep, tile0 * p.r, tail_full);
+        if (GATEUP) tma_load_2d(tail + p.r8 * ROW_BYTES, &p.tmW1t, p.KB * kstep, tile0 * p.r, tail_full);
+      }
       griddep_wait();
+      if (with_tail) tma_load_2d(tail + (GATEUP ? 2 : 1) * p.r8 * ROW_BYTES, &p.tmXt, p.KB * kstep, 0, tail_full);
       for (int t = tile0; t < p.tiles && !aborted; t += tile_step) {
         for (int ks = ks0; ks < ks1; ++ks) {
           const bool early = t == tile0 && ks < ks0 + ahead;
@@ -317,11 +302,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
           for (int t = blockIdx.x; t < p.next_tiles; t += gridDim.x)
             tma_prefetch_3d(&p.tmNext, 0, t * p.next_r, ks * p.next_s);
       if (*abort_flag) {
-        // every TMA this thread issued must land before the CTA exits
+        // every TMA this thread issued must land before the CTA exits (a stage whose tokens were not asked for any
+        // more never completes: the wait is bounded)
+        const uint64_t t0 = globaltimer_ns();
         for (int i = 0; i < p.stages; ++i)
           if (issued_mask & (1u << i)) {
             const uint32_t par = (issued_par >> i) & 1u;
-            const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(&full[i], par) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
             }
           }
@@ -422,6 +408,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
           }
         }
         if (aborted) break;
+        if (with_tail && me == 0) {
+          // into accumulators of its own: its operands' rows are not stacked
+          if (!mbar_wait(tail_full, 0, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t at = smem_desc_sw128(smem_u32(tail), 16, 1024), wt = p.r8 * ROW_BYTES >> 4;
+          const uint64_t bt = at + (GATEUP ? 2 : 1) * wt;
+          const uint32_t dt = tmem_base + p.acc_bufs * ISSUERS * p.acc_cols, idt = idesc<MX>(p.tail_n, 0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            mma_bf16(dt, at + 2 * q, bt + 2 * q, idt, q != 0 ? 1u : 0u);
+            if (two) mma_bf16(dt + p.tail_n, at + wt + 2 * q, bt + 2 * q, idt, q != 0 ? 1u : 0u);
+          }
+        }
         mma_commit(&tfull[acc]);
         if (++acc == p.acc_bufs) {
           acc = 0;
@@ -489,7 +491,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
         }
         cp_async_arrive(&sfull[st]);
       };
-      const int ahead = min(SF_SLOTS, ks1 - ks0);
+      // (a slot's arrival waits for every copy before it: not many stages ahead of the tokens' scales)
+      const int ahead = min(4, ks1 - ks0);
       for (int st = 0; st < ahead; ++st) weights(ks0 + st, st);
       griddep_wait();
       int slot = 0;
@@ -528,86 +531,60 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
       }
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + acc * ISSUERS * p.acc_cols;
+      const uint32_t tail_tb = tmem_base + ((uint32_t)(q * 32) << 16) + p.acc_bufs * ISSUERS * p.acc_cols;
       // with a single stage of K, only its issuer's accumulator holds something
       const bool both = ISSUERS == 2 && ks1 - ks0 > 1;
       const uint32_t tb1 = ISSUERS == 1 || both || !(iter++ & 1) ? tb : tb + p.acc_cols;
       const int n0 = t * p.r;
       const int rows = min(p.r, p.N - n0);
-      if (p.staged) {
-        // the parts of one element are on different lanes and columns: through shared memory (the ring, whose
-        // stages have all been read: a staged launch has one tile per CTA), fp32 [part][token][r], the parts
-        // being the K blocks of a stage, of W0 and then of W1
-        float* st = reinterpret_cast<float*>(ring);
-        for (int c = 0; c < p.s; ++c) {
-          for (int m = 0; m < (GATEUP ? 2 : 1); ++m) {
-            // this lane's operand row, as an index into block c of weight m
-            const int i = row - m * p.w_rows - c * p.r;
-            const bool mine = i >= 0 && i < p.r;
-            if (!__any_sync(0xffffffffu, mine)) continue;
-            const uint32_t col = tb1 + c * p.T;
-            for (int j = 16 * h; j < p.T; j += 32) {
-              float v[16], v2[16];
-              tmem_ld16(col + j, v);
-              if (both) tmem_ld16(col + p.acc_cols + j, v2);
-              tmem_ld_wait();
-              if (both)
-#pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] += v2[k];
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (mine && j + k < p.T) st[((m * p.s + c) * p.T + j + k) * p.r + i] = v[k];
-            }
-          }
+      if (p.staged) break;  // one tile per CTA, finished below
+      const bool ok = row < rows;
+      for (int c = 16 * h; c < p.T; c += 32) {
+        float v[16], u[16], v2[16], u2[16];
+        tmem_ld16(tb1 + c, v);
+        if (GATEUP) tmem_ld16(tb1 + p.mma_n + c, u);
+        if (both) {
+          tmem_ld16(tb + p.acc_cols + c, v2);
+          if (GATEUP) tmem_ld16(tb + p.acc_cols + p.mma_n + c, u2);
         }
-        if (CLUSTER && p.cs > 1) continue;  // finished below, with the other CTAs' parts
-        __syncwarp();
-        if (lane == 0) mbar_arrive(staged);
-        if (!__all_sync(0xffffffffu, mbar_wait(staged, 0, abort_flag, p.status, DEV_WAIT_TIMEOUT_EPILOGUE))) {
-          aborted = true;
-          break;
-        }
-        finish(t);
-      } else {
-        const bool ok = row < rows;
-        for (int c = 16 * h; c < p.T; c += 32) {
-          float v[16], u[16], v2[16], u2[16];
-          tmem_ld16(tb1 + c, v);
-          if (GATEUP) tmem_ld16(tb1 + p.mma_n + c, u);
-          if (both) {
-            tmem_ld16(tb + p.acc_cols + c, v2);
-            if (GATEUP) tmem_ld16(tb + p.acc_cols + p.mma_n + c, u2);
-          }
-          tmem_ld_wait();
-          if (both)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              v[i] += v2[i];
-              if (GATEUP) u[i] += u2[i];
-            }
+        tmem_ld_wait();
+        const auto add = [&] {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (c + i >= p.T) break;
-            const long long o = (long long)(c + i) * p.N + n0 + row;
-            if constexpr (GATEUP) {
-              const float a = swiglu::act(v[i], u[i]);
-              if (MX) {
-                uint8_t sb;
-                const uint8_t code = quant_lane(ok ? a : 0.f, sb);
-                if (ok) {
-                  static_cast<uint8_t*>(p.out)[o] = code;
-                  if (lane == 0) p.out_sf[o >> 5] = sb;
-                }
-              } else if (ok) {
-                static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a);
-                if (p.save) {
-                  __nv_bfloat16* sv = p.save + (long long)(c + i) * 2 * p.N + n0 + row;
-                  sv[0] = __float2bfloat16_rn(v[i]);
-                  sv[p.N] = __float2bfloat16_rn(u[i]);
-                }
+            v[i] += v2[i];
+            if (GATEUP) u[i] += u2[i];
+          }
+        };
+        if (both) add();
+        if (with_tail) {
+          tmem_ld16(tail_tb + c, v2);
+          if (GATEUP) tmem_ld16(tail_tb + p.tail_n + c, u2);
+          tmem_ld_wait();
+          add();
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (c + i >= p.T) break;
+          const long long o = (long long)(c + i) * p.N + n0 + row;
+          if constexpr (GATEUP) {
+            const float a = swiglu::act(v[i], u[i]);
+            if (MX) {
+              uint8_t sb;
+              const uint8_t code = quant_lane(ok ? a : 0.f, sb);
+              if (ok) {
+                static_cast<uint8_t*>(p.out)[o] = code;
+                if (lane == 0) p.out_sf[o >> 5] = sb;
               }
             } else if (ok) {
-              static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v[i]);
+              static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a);
+              if (p.save) {
+                __nv_bfloat16* sv = p.save + (long long)(c + i) * 2 * p.N + n0 + row;
+                sv[0] = __float2bfloat16_rn(v[i]);
+                sv[p.N] = __float2bfloat16_rn(u[i]);
+              }
             }
+          } else if (ok) {
+            static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v[i]);
           }
         }
       }
@@ -620,13 +597,115 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
       }
     }
   }
-  if (CLUSTER && p.cs > 1) {
-    // every CTA's parts are in its shared memory; it stays until the others have read them
+  if (p.staged) {
+    // The parts of one element (the K blocks of a stage, the tail, the CTAs of a cluster) are on different lanes,
+    // columns and SMs. The accumulators go to shared memory as they are (the ring, whose stages have all been read):
+    // fp32 [CTA][operand][column][128 rows], column c T + t of block c, token t; then the tails', [operand][t][128].
+    // The CTAs of a cluster divide the tokens: token t is finished by CTA t % cs, and the others write its columns
+    // into that CTA's memory.
+    const int cs = CLUSTER ? p.cs : 1, lc = cs >> 1;  // cs is 1, 2 or 4: its logarithm is cs / 2
+    const int ops = GATEUP && !p.merged ? 2 : 1;
+    const int Tl = (p.T + cs - 1) >> lc, cols = p.s * Tl;  // columns per CTA and operand, where they are finished
+    float* const tails = reinterpret_cast<float*>(ring) + (size_t)cs * ops * cols * 128;
     __syncwarp();
-    cluster_sync();
-    if (warp >= EPI_WARP0) finish(tile0);
-    __syncwarp();
-    cluster_sync();
+    if (CLUSTER && cs > 1) cluster_sync();  // every CTA's ring is free
+    if (warp >= EPI_WARP0) {
+      tc_fence_after();
+      const int q = warp & 3, h = (warp - EPI_WARP0) >> 2, row = 32 * q + lane;
+      const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16);
+      const bool both = ISSUERS == 2 && ks1 - ks0 > 1;
+      for (int op = 0; op < ops; ++op) {
+        for (int j = 16 * h; j < p.s * p.T; j += 32) {
+          float v[16];
+          tmem_ld16(tq + op * p.mma_n + j, v);
+          if (both) {
+            float v2[16];
+            tmem_ld16(tq + p.acc_cols + op * p.mma_n + j, v2);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] += v2[k];
+          } else {
+            tmem_ld_wait();
+          }
+          if (!CLUSTER || cs == 1) {
+            float* dst = reinterpret_cast<float*>(ring) + ((size_t)op * cols + j) * 128 + row;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (j + k < cols) dst[128 * k] = v[k];
+          } else {
+            int c = j / p.T, tok = j - c * p.T;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              if (c < p.s) {
+                const uint32_t at = ((uint32_t)((rank * ops + op) * cols + c * Tl + (tok >> lc)) * 128 + row) * 4;
+                st_cluster(cluster_addr(smem_u32(ring), tok & (cs - 1)) + at, v[k]);
+              }
+              if (++tok == p.T) {
+                tok = 0;
+                ++c;
+              }
+            }
+          }
+        }
+        if (with_tail) {
+          for (int j = 16 * h; j < p.T; j += 32) {
+            float v[16];
+            tmem_ld16(tq + ISSUERS * p.acc_cols + op * p.tail_n + j, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int tok = j + k;
+              if (tok >= p.T) break;
+              const uint32_t at = smem_u32(tails + (size_t)(op * Tl + (tok >> lc)) * 128 + row);
+              st_cluster(cs > 1 ? cluster_addr(at, tok & (cs - 1)) : at, v[k]);
+            }
+          }
+        }
+      }
+    }
+    if (CLUSTER && cs > 1) cluster_sync();
+    else __syncthreads();
+    // a warp takes 32 columns of one token at a time, and adds the parts in the order of K
+    const int n0 = tile0 * p.r, rows = min(p.r, p.N - n0);
+    const int mine = (p.T - rank + cs - 1) >> lc;  // tokens of this CTA
+    const int up = p.merged ? p.w_rows : cols * 128, up_tail = p.merged ? p.r8 : Tl * 128;
+    for (int f0 = 0; f0 < rows; f0 += 32) {
+      const int f = f0 + lane;
+      const bool ok = f < rows;
+      const float* st = reinterpret_cast<const float*>(ring) + (ok ? f : 0);
+      for (int tl = warp; tl < mine; tl += NUM_THREADS / 32) {
+        float g = 0.f, u = 0.f;
+        for (int k = 0; k < cs; ++k) {
+          const float* pt = st + ((size_t)k * ops * cols + tl) * 128;
+          for (int c = 0; c < p.s; ++c, pt += Tl * 128 + p.r) {
+            g += pt[0];
+            if (GATEUP) u += pt[up];
+          }
+        }
+        if (!MX && p.tail) {
+          const float* pt = tails + (size_t)tl * 128 + (ok ? f : 0);
+          g += pt[0];
+          if (GATEUP) u += pt[up_tail];
+        }
+        const float a = GATEUP ? swiglu::act(g, u) : g;
+        const long long tok = (tl << lc) + rank, o = tok * p.N + n0 + f;
+        if (MX && GATEUP) {
+          uint8_t sb;
+          const uint8_t code = quant_lane(ok ? a : 0.f, sb);
+          if (ok) {
+            static_cast<uint8_t*>(p.out)[o] = code;
+            if (lane == 0) p.out_sf[o >> 5] = sb;
+          }
+        } else if (ok) {
+          static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a);
+          if (GATEUP && p.save) {
+            __nv_bfloat16* sv = p.save + tok * 2 * p.N + n0 + f;
+            sv[0] = __float2bfloat16_rn(g);
+            sv[p.N] = __float2bfloat16_rn(u);
+          }
+        }
+      }
+    }
   }
   __syncthreads();
   if (warp == 1) {
@@ -639,36 +718,63 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
 // (boxes of 128 bytes x r rows, or T tokens, x s blocks).
 template <bool MX, bool GATEUP>
 Params plan(int T, int N, int K) {
-  constexpr int ISSUERS = issuers(MX);
+  constexpr int ISSUERS = issuers(MX, GATEUP);
   Params p{};
   p.T = T;
   p.N = N;
   p.K = K;
   const int kstep = MX ? 128 : 64;
-  p.KB = (K + kstep - 1) / kstep;
-  p.z = K % kstep == 0;
   const int sms = moe_host::num_sms();
   // equal tiles of at most 128 rows, in as few rounds over the SMs as that allows; the MXFP8 activation's blocks
   // of 32 columns stay within a tile
   const int unit = MX && GATEUP ? 32 : 8;
-  const int rounds = (N + 128 * sms - 1) / (128 * sms);
-  p.r = (N + rounds * sms - 1) / (rounds * sms);
-  if (MX && GATEUP) p.r = (p.r + 31) / 32 * 32;
-  if (p.r < unit) p.r = unit;
-  p.tiles = (N + p.r - 1) / p.r;
-  const bool one = p.tiles <= sms;  // one tile per CTA
-  const auto rows8 = [&](int s) { return (s * p.r + 7) / 8 * 8; };
-  p.s = 1;
-  const int most = GATEUP ? 64 : 128;  // operand rows of one weight
-  if (one && p.z)
-    while (2 * p.s <= (MX ? 4 : 8) && rows8(2 * p.s) <= most && 2 * p.s * T <= MAX_N && 2 * p.s <= p.KB) p.s *= 2;
-  p.w_rows = rows8(p.s);
-  p.merged = GATEUP && one && p.w_rows <= most;
-  p.staged = p.merged || p.s > 1;
-  p.KS = (p.KB + p.s - 1) / p.s;
-  p.mma_n = (p.s * T + 15) / 16 * 16;
+  const auto cut = [&](int n) {  // over n CTAs or clusters
+    const int rounds = (N + 128 * n - 1) / (128 * n);
+    p.r = (N + rounds * n - 1) / (rounds * n);
+    if (MX && GATEUP) p.r = (p.r + 31) / 32 * 32;
+    if (p.r < unit) p.r = unit;
+    p.tiles = (N + p.r - 1) / p.r;
+  };
+  cut(sms);
   p.cs = 1;
-  if (MX && p.merged)
+  // Every CTA reads all tokens' K range. Where that is more than the weights it streams, two share a tile of twice
+  // the rows and half of K each (48 tokens, H = 4096, F = 14336: 202 MB of activations through L2 next to 117 MB of
+  // down weights, halved).
+  if (!GATEUP && p.tiles <= sms && 4 * T > 5 * p.r && K >= 32 * kstep) {
+    p.cs = 2;
+    cut(sms / 2);
+  }
+  p.r8 = (p.r + 7) / 8 * 8;
+  const bool one = p.tiles * p.cs <= sms;  // one tile per CTA
+  p.tail = one && K > kstep ? K % kstep : 0;
+  p.tail_n = (T + 15) / 16 * 16;
+  p.z = p.tail || K % kstep == 0;
+  p.KB = p.z ? K / kstep : (K + kstep - 1) / kstep;
+  // K blocks per stage, and gate and up in one operand or in two: what costs the MMA issuer least per block (a wait
+  // and a commit 150 ns, an MMA 32 + N / 8, a copy of scales 60), as far as operand rows, TMEM and the ring allow
+  float best = 1e30f;
+  for (int merged = 0; merged <= (GATEUP && one ? 1 : 0); ++merged)
+    for (int s = 1; s <= (one && p.z ? (MX ? 4 : MAX_PARTS - 1) : 1); s += MX ? s : 1) {
+      const int rows = (s * p.r + 7) / 8 * 8, n = (s * T + 15) / 16 * 16, ops = GATEUP && !merged ? 2 : 1;
+      if (rows * (merged ? 2 : 1) > 128 || (s > 1 && (s * T > MAX_N || s > p.KB))) continue;
+      const int stage = (GATEUP ? 2 : 1) * rows * ROW_BYTES + n * ROW_BYTES;
+      const int cols = ISSUERS * ops * n + (MX ? 2 * ISSUERS * SF_SLOT_COLS : 16) + (p.tail ? ops * p.tail_n : 0);
+      if (s > 1 && (cols > 512 || 4 * stage > RING_ALONE - (MX ? SF_SLOTS * 2048 : 40 * 1024))) continue;
+      // a staged epilogue's accumulators fit where the ring (four stages at least) was
+      if ((s > 1 || merged) && 512 * ops * (s * (T + MAX_CLUSTER - 1) + (p.tail ? T + 1 : 0)) > 4 * stage) continue;
+      const float cost = (150.f + 4 * ops * (32.f + n / 8.f) + (MX ? 60.f * (ops + 1) : 0.f)) / s;
+      if (cost < best) {
+        best = cost;
+        p.s = s;
+        p.merged = merged;
+        p.w_rows = rows;
+        p.mma_n = n;
+      }
+    }
+  p.staged = p.merged || p.s > 1 || p.cs > 1;
+  p.KS = (p.KB + p.s - 1) / p.s;
+  p.tail_bytes = p.tail ? ((GATEUP ? 2 : 1) * p.r8 + p.tail_n) * ROW_BYTES : 0;
+  if (MX && GATEUP && p.staged)
     while (2 * p.cs <= MAX_CLUSTER && 2 * p.cs * p.tiles <= sms && p.KS >= 8 * p.cs) p.cs *= 2;
   p.stage_bytes = (GATEUP ? 2 : 1) * p.w_rows * ROW_BYTES + p.mma_n * ROW_BYTES;
   p.sf_w1 = p.merged ? 0 : 512;
@@ -676,14 +782,17 @@ Params plan(int T, int N, int K) {
   p.sf_bytes = p.sf_x + (p.mma_n + 127) / 128 * 512;
   const int sf_ring = MX ? SF_SLOTS * p.sf_bytes : 0;
   const long long all = (long long)p.KS / p.cs * p.stage_bytes * ((p.tiles + sms - 1) / sms);
-  p.stages = ((GATEUP ? RING_GATEUP : RING_DOWN) - sf_ring) / p.stage_bytes;
-  if (p.stages < 4 || all > SHORT_BYTES) p.stages = (RING_ALONE - sf_ring) / p.stage_bytes;
+  const int used = sf_ring + p.tail_bytes;
+  p.stages = ((GATEUP ? RING_GATEUP : RING_DOWN) - used) / p.stage_bytes;
+  if (p.stages < 4 || all > SHORT_BYTES) p.stages = (RING_ALONE - used) / p.stage_bytes;
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   p.stages -= p.stages % ISSUERS;
   const int reach = (GATEUP && !p.merged ? p.w_rows * ROW_BYTES : 0) + OPERAND_BYTES;  // of the operands of a stage
   p.ring_bytes = p.stages * p.stage_bytes + (reach > p.stage_bytes ? reach - p.stage_bytes : 0);
   p.acc_cols = (GATEUP && !p.merged ? 2 : 1) * p.mma_n;
-  const int more = MX ? 2 * ISSUERS * SF_SLOT_COLS : p.s > 1 ? 16 : 0;  // 16: what a last read may pass them by
+  // past the accumulators: the scales, or the tail's, or what a last read may pass them by
+  const int more = MX ? 2 * ISSUERS * SF_SLOT_COLS
+                      : p.tail ? (GATEUP && !p.merged ? 2 : 1) * p.tail_n + 16 : p.s > 1 ? 16 : 0;
   p.acc_bufs = one || 2 * ISSUERS * p.acc_cols + more > 512 ? 1 : 2;
   const int cols = p.acc_bufs * ISSUERS * p.acc_cols + more;
   p.tmem_cols = 32;
@@ -701,13 +810,21 @@ bool encode_map(CUtensorMap* m, const Params& p, const void* base, int rows, int
                                   p.s);
 }
 
+// The maps of one operand: the whole blocks, and the tail.
+template <bool MX>
+bool encode_maps(CUtensorMap* m, CUtensorMap* mt, const Params& p, const void* base, int rows, int box) {
+  if (!encode_map<MX>(m, p, base, rows, box)) return false;
+  return !p.tail || moe_host::encode_tmap_2d(mt, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, p.K, rows, (uint64_t)p.K * 2,
+                                             64, box);
+}
+
 // The weights [K, N] of the down product that follows a gate/up launch: up to NEXT_BYTES of them beyond what its
 // ring takes are asked into L2 (about what memory delivers while the one kernel ends and the other begins).
 constexpr long long NEXT_BYTES = 48ll << 20;
 template <bool MX>
 bool plan_next(Params& p, const void* W_next) {
   const Params d = plan<MX, false>(p.T, p.K, p.N);
-  if (!d.z) return true;  // ragged K: one small box per stage, not worth it
+  if (!d.z) return true;  // small boxes of one block, not worth it
   p.next_r = d.r;
   p.next_s = d.s;
   p.next_tiles = d.tiles;
@@ -719,7 +836,8 @@ bool plan_next(Params& p, const void* W_next) {
 
 // dep: the kernel before it in the stream is one of the same call's (the weights are not its results).
 template <bool MX, bool GATEUP>
-int launch(const Params& p, cudaStream_t st, bool dep) {
+int launch(Params& p, cudaStream_t st, bool dep) {
+  p.early = dep;
   auto kern = gemm_kernel<MX, GATEUP>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_ALONE + OPERAND_BYTES + SMEM_FIXED) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -729,7 +847,7 @@ int launch(const Params& p, cudaStream_t st, bool dep) {
   const int sms = moe_host::num_sms();
   cfg.gridDim = dim3(p.cs > 1 ? p.tiles * p.cs : p.tiles < sms ? p.tiles : sms);
   cfg.blockDim = dim3(NUM_THREADS);
-  cfg.dynamicSmemBytes = p.ring_bytes + (MX ? SF_SLOTS * p.sf_bytes : 0) + SMEM_FIXED;
+  cfg.dynamicSmemBytes = p.tail_bytes + p.ring_bytes + (MX ? SF_SLOTS * p.sf_bytes : 0) + SMEM_FIXED;
   cfg.stream = st;
   cudaLaunchAttribute at[2] = {};
   int n = 0;

@@ -10,7 +10,7 @@ BF = torch.bfloat16
 # (T, H, F): both sides of every choice by the number of tokens, odd sizes, tails of a tile and of a k-block, many
 # tiles with a rest, one tile
 SHAPES = [(1, 8, 8), (1, 256, 512), (1, 2056, 1544), (3, 1000, 264), (8, 520, 1040), (9, 256, 384), (16, 136, 4104),
-          (17, 264, 200), (31, 2048, 768), (33, 1032, 136), (48, 2056, 1544), (64, 1032, 1160), (65, 1032, 1160),
+          (17, 264, 200), (31, 2048, 768), (33, 1032, 136), (48, 2056, 1544), (64, 1032, 1160), (60, 1032, 2312), (50, 520, 4096), (65, 1032, 1160),
           (65, 256, 512), (2, 136, 9480), (40, 264, 19208), (64, 19016, 136), (1, 4096, 9600), (3, 320, 19208),
           (2, 64, 19208), (5, 19016, 320), (2, 19016, 64), (127, 72, 200), (128, 384, 640), (129, 136, 1032), (200, 8, 8), (257, 520, 2568), (300, 2048, 4104),
           (1001, 1288, 1160), (1500, 2568, 3592)]
