@@ -19,7 +19,9 @@ def __getattr__(name):
         if name in _SUBMODULES:
             return importlib.import_module(f"{__name__}.{name}")
         raise AttributeError(name)
-    return getattr(importlib.import_module(f"{__name__}.binding"), name)
+    value = getattr(importlib.import_module(f"{__name__}.binding"), name)
+    globals()[name] = value  # found directly from now on
+    return value
 
 
 def load():

@@ -105,6 +105,8 @@ def lib_path() -> str:
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load the CUDA library (building it in-tree with nvcc if it is absent or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if build_if_missing and not _build.up_to_date():
@@ -138,8 +140,28 @@ def _p(t):
 
 def _st(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle, without building a torch.cuda.Stream (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
+
+
+def _ps(*tensors):
+    """Pointers of device tensors (or None) that must all live on the current device, where the call launches."""
+    dev = torch._C._cuda_getDevice()
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+        assert t.is_contiguous()
+        out.append(t.data_ptr())
+    return out
+
+
+def _nbytes(ws):
+    return ws.numel() * ws.element_size() if ws is not None else 0
 
 
 def _check(fn, rc):
@@ -347,8 +369,7 @@ def moe_rmsnorm_fwd(x, residual, weight, eps, h, y, y_q, y_sf, rstd, stream=None
     """x, residual [..., H] bf16 (residual or None); outputs h, y, y_q + y_sf, rstd may each be None."""
     H = x.shape[-1]
     return _check("moe_rmsnorm_fwd", load().moe_rmsnorm_fwd(
-        x.numel() // H, H, _p(x), _p(residual), _p(weight), eps, _p(h), _p(y), _p(y_q), _p(y_sf), _p(rstd),
-        _st(stream)))
+        x.numel() // H, H, *_ps(x, residual, weight), eps, *_ps(h, y, y_q, y_sf, rstd), _st(stream)))
 
 
 def moe_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
@@ -356,10 +377,10 @@ def moe_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
 
 
 def moe_rmsnorm_bwd(dY, h, weight, rstd, dh, dX, dweight, ws, stream=None):
+    """dh (the upstream of h), dX, dweight may be None; ws only with dweight."""
     H = h.shape[-1]
     return _check("moe_rmsnorm_bwd", load().moe_rmsnorm_bwd(
-        h.numel() // H, H, _p(dY), _p(h), _p(weight), _p(rstd), _p(dh), _p(dX), _p(dweight), _p(ws),
-        ws.numel() if ws is not None else 0, _st(stream)))
+        h.numel() // H, H, *_ps(dY, h, weight, rstd, dh, dX, dweight, ws), _nbytes(ws), _st(stream)))
 
 
 def make_ffn_config(T, H, F, dtype="bf16", save_for_bwd=0) -> moe_ffn_config:
@@ -377,8 +398,8 @@ def moe_ffn_saved_size(cfg) -> int:
 
 def moe_ffn_fwd(cfg, x, x_sf, W_g, W_u, W_d, W_g_sf, W_u_sf, W_d_sf, y, saved, ws, stream=None):
     return _check("moe_ffn_fwd", load().moe_ffn_fwd(
-        ctypes.byref(cfg), _p(x), _p(x_sf), _p(W_g), _p(W_u), _p(W_d), _p(W_g_sf), _p(W_u_sf), _p(W_d_sf), _p(y),
-        _p(saved), _p(ws), ws.numel() if ws is not None else 0, _st(stream)))
+        ctypes.byref(cfg), *_ps(x, x_sf, W_g, W_u, W_d, W_g_sf, W_u_sf, W_d_sf, y, saved, ws), _nbytes(ws),
+        _st(stream)))
 
 
 def moe_ffn_bwd_workspace_size(cfg) -> int:
@@ -386,6 +407,6 @@ def moe_ffn_bwd_workspace_size(cfg) -> int:
 
 
 def moe_ffn_bwd(cfg, dY, x, W_g, W_u, W_d, saved, dX, dW_g, dW_u, dW_d, ws, stream=None):
+    """dX, the pair dW_g and dW_u, and dW_d may each be None (not all)."""
     return _check("moe_ffn_bwd", load().moe_ffn_bwd(
-        ctypes.byref(cfg), _p(dY), _p(x), _p(W_g), _p(W_u), _p(W_d), _p(saved), _p(dX), _p(dW_g), _p(dW_u), _p(dW_d),
-        _p(ws), ws.numel() if ws is not None else 0, _st(stream)))
+        ctypes.byref(cfg), *_ps(dY, x, W_g, W_u, W_d, saved, dX, dW_g, dW_u, dW_d, ws), _nbytes(ws), _st(stream)))

@@ -27,6 +27,8 @@
 // order of K and applies the epilogue, so results do not depend on timing.
 #pragma once
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "swiglu.cuh"
 
@@ -549,11 +551,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
   }
 }
 
-// Adds the partial accumulators of every tile that was cut (in the order of K) and applies the epilogue.
-// Thread: one row and 8 output columns; grid.x: tiles, grid.y: column groups of CTA_COLS.
+// Adds the partial accumulators of every tile that was cut (at most MAX_PIECES) and applies the epilogue. Item: one
+// row and 8 output columns; grid.x: tiles. With many pieces, SPLIT = 4 threads take every fourth, and are added in
+// a fixed order (8 tiles in 18 pieces each: 17 us by one thread; 64 tiles in 2 or 3: 14 by four, 10.7 by one).
 constexpr int FIX_THREADS = 256;
-template <int OP, int CG>
+constexpr int MAX_PIECES = 16, MANY_PIECES = 6;
+template <int OP, int CG, int SPLIT>
 __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constant__ Params p) {
+  constexpr int NV = OP == OP_GATEUP ? 16 : 8, FIX_ITEMS = FIX_THREADS / SPLIT;
+  __shared__ float sums[SPLIT > 1 ? SPLIT - 1 : 1][NV][FIX_ITEMS];
   griddep_wait();
   griddep_launch_dependents();
   const int i = blockIdx.x / CG, rank = CG == 2 ? (int)blockIdx.x & 1 : 0;
@@ -561,22 +567,44 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
   if (b0 == b1) return;  // one CTA (pair) held the whole tile and finished it
   const Origin o = origin<OP, CG>(p, p.n_full + i, rank);
   if (o.rows <= 0) return;
-  const int groups = (o.cols + 7) / 8;
-  for (int e = blockIdx.y * FIX_THREADS + threadIdx.x; e < groups * o.rows; e += gridDim.y * FIX_THREADS) {
-    const int r = e % o.rows, c = 8 * (e / o.rows);
+  const int part = threadIdx.x / FIX_ITEMS, item = threadIdx.x % FIX_ITEMS;
+  const int total = (o.cols + 7) / 8 * o.rows;
+  for (int e0 = blockIdx.y * FIX_ITEMS; e0 < total; e0 += gridDim.y * FIX_ITEMS) {  // the same for the whole CTA
+    const int e = e0 + item, r = e % o.rows, c = 8 * (e / o.rows);
     float v[8], u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
+    if (e < total) {
 #pragma unroll 4
-    for (int b = b0; b <= b1; ++b) {
-      const int slot = 2 * b + (b * p.sk_per > i * p.KB ? 0 : 1);
-      const float* src = p.part + (size_t)(slot * CG + rank) * SLOT_FLOATS + (size_t)c * BM + r;
+      for (int b = b0 + part; b <= b1; b += SPLIT) {
+        const int slot = 2 * b + (b * p.sk_per > i * p.KB ? 0 : 1);
+        const float* src = p.part + (size_t)(slot * CG + rank) * SLOT_FLOATS + (size_t)c * BM + r;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] += src[j * BM];
-        if (OP == OP_GATEUP) u[j] += src[(BN / 2 + j) * BM];
+        for (int j = 0; j < 8; ++j) {
+          v[j] += src[j * BM];
+          if (OP == OP_GATEUP) u[j] += src[(BN / 2 + j) * BM];
+        }
       }
     }
+    if constexpr (SPLIT > 1) {
+      __syncthreads();  // the last round's sums have been read
+      if (part > 0)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sums[part - 1][j][item] = v[j];
+          if (OP == OP_GATEUP) sums[part - 1][(NV - 8) + j][item] = u[j];
+        }
+      __syncthreads();
+      if (part == 0)
+#pragma unroll
+        for (int s = 0; s < SPLIT - 1; ++s)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            v[j] += sums[s][j][item];
+            if (OP == OP_GATEUP) u[j] += sums[s][(NV - 8) + j][item];
+          }
+    }
+    if (part > 0 || e >= total) continue;
     const long long row = o.m0 + r;
     const auto pack = [](const float (&t)[8]) {
       return make_uint4(pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3]), pack_bf16x2(t[4], t[5]),
@@ -681,13 +709,16 @@ int launch_cg(Params& p, int workers, cudaStream_t st, bool dep) {
   const bool cut = rest && (long long)(workers - rest) * p.KB > (p.ragged ? 9ll : 22ll) * workers;
   p.n_full = (int)(cut ? total - rest : total);
   p.sk_tiles = cut ? rest : 0;
-  p.sk_per = cut ? (rest * p.KB + workers - 1) / workers : 0;
+  p.sk_per = cut ? std::max((rest * p.KB + workers - 1) / workers, (p.KB + MAX_PIECES - 1) / MAX_PIECES) : 0;
   auto kern = gemm_kernel<OP, CG>;
   int n = workers;
   if (!cut && total < n) n = (int)total;
   int rc = launch_dep(kern, dim3(n * CG), NUM_THREADS, C::SMEM_BYTES, CG, st, p, dep);
   if (rc || !cut) return rc;
-  return launch_dep(fixup_kernel<OP, CG>, dim3(rest * CG, OP == OP_GATEUP ? 8 : 16), FIX_THREADS, 0, 1, st, p, true);
+  const int per_tile = OP == OP_GATEUP ? 8 : 16;  // CTAs, one item per thread
+  if (p.KB > MANY_PIECES * p.sk_per)
+    return launch_dep(fixup_kernel<OP, CG, 4>, dim3(rest * CG, 4 * per_tile), FIX_THREADS, 0, 1, st, p, true);
+  return launch_dep(fixup_kernel<OP, CG, 1>, dim3(rest * CG, per_tile), FIX_THREADS, 0, 1, st, p, true);
 }
 
 // dep: the kernel before it in the stream is one of the same call's.

@@ -18,6 +18,9 @@ namespace rms {
 
 constexpr int MAX_THREADS = 512;
 constexpr int MAX_H = 16384;  // MAX_THREADS x 4 vectors of 8
+// CTAs of the backward, each of which leaves one row of partial dweight: two per SM of a B200. A constant, so that
+// the workspace does not depend on the device that is current.
+constexpr int BWD_CTAS = 2 * 148;
 
 MOE_DEV uint4 ld_stream(const __nv_bfloat16* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 // bf16 pair -> fp32 is a shift: element 2i in the low half of word i
@@ -153,6 +156,7 @@ __global__ void __launch_bounds__(MAX_THREADS) bwd_kernel(const BwdParams p) {
   __shared__ float red[2][16];
   const int nvec = p.H >> 3;
   const int nwarp = blockDim.x >> 5;
+  griddep_launch_dependents();
   uint4 w[V], ny[V], nh[V], nd[V];
   float nr;
   bool ok[V];
@@ -226,23 +230,32 @@ __global__ void __launch_bounds__(MAX_THREADS) bwd_kernel(const BwdParams p) {
   }
 }
 
-// dweight[c] = sum over the CTAs' partials, in a fixed order: 32 columns per CTA, 8 warps over the partials.
-__global__ void __launch_bounds__(256) dweight_kernel(const float* __restrict__ part, int n, int H,
-                                                      float* __restrict__ dw) {
-  __shared__ float s[8][32];
+// dweight[c] = sum over the CTAs' partials, in a fixed order: 32 columns per CTA, whose 32 warps take every 32nd
+// partial each (at most ten, all loaded at once) before the warps' sums are added.
+constexpr int DW_WARPS = 32;
+__global__ void __launch_bounds__(32 * DW_WARPS) dweight_kernel(const float* __restrict__ part, int n, int H,
+                                                                float* __restrict__ dw) {
+  __shared__ float s[DW_WARPS][33];
+  griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  constexpr int PER = (BWD_CTAS + DW_WARPS - 1) / DW_WARPS;
+  float v[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int r = warp + i * DW_WARPS;
+    v[i] = c < H && r < n ? part[(long long)r * H + c] : 0.f;
+  }
   float a = 0.f;
-  if (c < H)
-    for (int i = warp; i < n; i += 8) a += part[(long long)i * H + c];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) a += v[i];
   s[warp][lane] = a;
   __syncthreads();
-  if (warp == 0 && c < H) {
-    float t = 0.f;
+  // warp w adds column w of the tile
+  a = s[lane][warp];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += s[i][lane];
-    dw[c] = t;
-  }
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < H) dw[blockIdx.x * 32 + warp] = a;
 }
 
 // Vectors per thread and threads per row.
@@ -257,9 +270,7 @@ static Shape shape_of(int T, int H, bool bwd) {
   return {v, ((nvec + v - 1) / v + 31) / 32 * 32};
 }
 
-// CTAs of the backward, each of which leaves one row of partial dweight: two per SM of a B200, at least one
-// token each. A constant, so that the workspace does not depend on the device that is current.
-static int bwd_ctas(int T) { return T < 2 * 148 ? T : 2 * 148; }
+static int bwd_ctas(int T) { return T < BWD_CTAS ? T : BWD_CTAS; }
 
 static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -338,8 +349,20 @@ extern "C" int moe_rmsnorm_bwd(int32_t T, int32_t H, const void* dY, const void*
   }
   MOE_CHECK_LAUNCH();
   if (dweight) {
-    dweight_kernel<<<(H + 31) / 32, 256, 0, st>>>(p.part, grid, H, dweight);
-    MOE_CHECK_LAUNCH();
+    // launched while the backward kernel runs; it waits for it
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((H + 31) / 32);
+    cfg.blockDim = dim3(32 * DW_WARPS);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, dweight_kernel, (const float*)p.part, grid, (int)H, dweight) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
   }
   return MOE_OK;
 }

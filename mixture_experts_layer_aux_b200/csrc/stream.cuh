@@ -839,7 +839,8 @@ template <bool MX, bool GATEUP>
 int launch(Params& p, cudaStream_t st, bool dep) {
   p.early = dep;
   auto kern = gemm_kernel<MX, GATEUP>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_ALONE + OPERAND_BYTES + SMEM_FIXED) != cudaSuccess) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           RING_ALONE + OPERAND_BYTES + SMEM_FIXED) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }

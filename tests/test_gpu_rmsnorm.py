@@ -128,8 +128,8 @@ def test_backward(moe, T, H, dh):
         terms = terms + c[4].double().abs()
     d = (dx[:T].double().cpu() - rx).abs()
     assert bool((d <= U * rx.abs() + REL * terms).all()), float((d / (U * rx.abs() + REL * terms)).max())
-    # dweight: at most T / 296 + 1 rows, 37 partials and 8 sums in a row
-    depth = T / 296 + 1 + 37 + 8 + 3
+    # dweight: at most T / 296 + 1 rows, ten partials and five levels of sums in a row
+    depth = T / 296 + 1 + 10 + 5 + 3
     tw = (c[0].double().abs() * xhat).sum(0)
     assert bool(((dw.double().cpu() - rw).abs() <= depth * F32 * tw).all())
 
