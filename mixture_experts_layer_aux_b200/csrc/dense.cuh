@@ -70,8 +70,12 @@ struct __align__(64) Params {
   __nv_bfloat16* C;
   __nv_bfloat16* C2;
   long long ldc;
-  __nv_bfloat16* save;            // OP_GATEUP: [M, 2N] gate | up, or NULL
-  const __nv_bfloat16* gateup;    // OP_DGRAD_ACT: the same, as saved
+  // Saved pre-activations (swiglu.cuh), written by OP_GATEUP (NULL: not kept) and read by OP_DGRAD_ACT, whose dgate |
+  // dup have the same shape: rows of ld2 elements, up in columns `up` on
+  __nv_bfloat16* save_hi;
+  uint8_t* save_lo;
+  long long ld2;
+  int up;
   int* status;
 };
 
@@ -264,12 +268,59 @@ MOE_DEV void load_rows(uint8_t* stg, uint32_t (&w)[16], const __nv_bfloat16* src
   __syncwarp();
 }
 
+// The same for 32 bytes of each row (8 words per lane, 4 lanes x 8 bytes per row).
+MOE_DEV void store_rows8(uint8_t* stg, const uint32_t (&w)[8], uint8_t* dst, long long ld, int rows, int cols) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    *reinterpret_cast<uint4*>(stg + lane * STG_ROW + 16 * j) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  __syncwarp();
+  const int piece = lane & 3, r0 = lane >> 2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + r0;
+    if (r < rows && 8 * piece < cols)
+      *reinterpret_cast<uint2*>(dst + r * ld + 8 * piece) = *reinterpret_cast<const uint2*>(stg + r * STG_ROW + 8 * piece);
+  }
+  __syncwarp();
+}
+MOE_DEV void load_rows8(uint8_t* stg, uint32_t (&w)[8], const uint8_t* src, long long ld, int rows, int cols) {
+  const int lane = threadIdx.x & 31;
+  const int piece = lane & 3, r0 = lane >> 2;
+  uint2 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + r0;
+    v[i] = make_uint2(0, 0);
+    if (r < rows && 8 * piece < cols) v[i] = *reinterpret_cast<const uint2*>(src + r * ld + 8 * piece);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint2*>(stg + (8 * i + r0) * STG_ROW + 8 * piece) = v[i];
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint4 u = *reinterpret_cast<const uint4*>(stg + lane * STG_ROW + 16 * j);
+    w[4 * j] = u.x;
+    w[4 * j + 1] = u.y;
+    w[4 * j + 2] = u.z;
+    w[4 * j + 3] = u.w;
+  }
+  __syncwarp();
+}
+MOE_DEV void split32(const float (&v)[32], uint32_t (&hi)[16], uint32_t (&lo)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    hi[2 * i] = swiglu::hi2(v[4 * i], v[4 * i + 1]);
+    hi[2 * i + 1] = swiglu::hi2(v[4 * i + 2], v[4 * i + 3]);
+    lo[i] = swiglu::lo4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+}
+
 MOE_DEV void pack32(const float (&v)[32], uint32_t (&w)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
 }
-MOE_DEV float word_lo(uint32_t w) { return __uint_as_float(w << 16); }
-MOE_DEV float word_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 template <int OP, int CG>
 __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_constant__ Params p) {
@@ -473,7 +524,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
             for (int i = 0; i < 32; ++i) dst[(size_t)(c + i) * BM] = v[i];
         }
       } else if constexpr (OP == OP_GATEUP) {
-        const long long ld2 = 2LL * p.N;
 #pragma unroll 1
         for (int c = h * 64; c < (h + 1) * 64; c += 32) {
           const int cols = o.cols - c;
@@ -483,12 +533,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
           tmem_ld32(tb + c, g);
           tmem_ld32(tb + BN / 2 + c, u);
           tmem_ld_wait();
-          if (p.save) {
-            __nv_bfloat16* sv = p.save + row0 * ld2 + o.n0 + c;
-            pack32(g, w);
-            store_rows(stg, w, sv, ld2, rows, cols);
-            pack32(u, w);
-            store_rows(stg, w, sv + p.N, ld2, rows, cols);
+          if (p.save_hi) {
+            const long long at = row0 * p.ld2 + o.n0 + c;
+            uint32_t lo[8];
+            split32(g, w, lo);
+            store_rows(stg, w, p.save_hi + at, p.ld2, rows, cols);
+            store_rows8(stg, lo, p.save_lo + at, p.ld2, rows, cols);
+            split32(u, w, lo);
+            store_rows(stg, w, p.save_hi + at + p.up, p.ld2, rows, cols);
+            store_rows8(stg, lo, p.save_lo + at + p.up, p.ld2, rows, cols);
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) g[i] = swiglu::act(g[i], u[i]);
@@ -496,29 +549,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
           store_rows(stg, w, p.C + row0 * p.ldc + o.n0 + c, p.ldc, rows, cols);
         }
       } else if constexpr (OP == OP_DGRAD_ACT) {
-        const long long ld2 = 2LL * p.N;
 #pragma unroll 1
         for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
           const int cols = o.cols - c;
           if (cols <= 0) break;
           float v[32];
-          uint32_t zg[16], zu[16];
-          const __nv_bfloat16* src = p.gateup + row0 * ld2 + o.n0 + c;
-          load_rows(stg, zg, src, ld2, rows, cols);
-          load_rows(stg, zu, src + p.N, ld2, rows, cols);
+          uint32_t zg[16], zu[16], lg[8], lu[8];
+          const long long at = row0 * p.ld2 + o.n0 + c;
+          load_rows(stg, zg, p.save_hi + at, p.ld2, rows, cols);
+          load_rows8(stg, lg, p.save_lo + at, p.ld2, rows, cols);
+          load_rows(stg, zu, p.save_hi + at + p.up, p.ld2, rows, cols);
+          load_rows8(stg, lu, p.save_lo + at + p.up, p.ld2, rows, cols);
           tmem_ld32(tb + c, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float g0, u0, g1, u1;
-            swiglu::grad(v[2 * i], word_lo(zg[i]), word_lo(zu[i]), g0, u0);
-            swiglu::grad(v[2 * i + 1], word_hi(zg[i]), word_hi(zu[i]), g1, u1);
-            zg[i] = pack_bf16x2(g0, g1);
-            zu[i] = pack_bf16x2(u0, u1);
+          for (int i = 0; i < 8; ++i) {
+            float g[4], u[4];
+            swiglu::join4(zg[2 * i], zg[2 * i + 1], lg[i], g);
+            swiglu::join4(zu[2 * i], zu[2 * i + 1], lu[i], u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) swiglu::grad(v[4 * i + j], g[j], u[j], g[j], u[j]);
+            zg[2 * i] = pack_bf16x2(g[0], g[1]);
+            zg[2 * i + 1] = pack_bf16x2(g[2], g[3]);
+            zu[2 * i] = pack_bf16x2(u[0], u[1]);
+            zu[2 * i + 1] = pack_bf16x2(u[2], u[3]);
           }
-          __nv_bfloat16* dst = p.C + row0 * ld2 + o.n0 + c;
-          store_rows(stg, zg, dst, ld2, rows, cols);
-          store_rows(stg, zu, dst + p.N, ld2, rows, cols);
+          store_rows(stg, zg, p.C + at, p.ld2, rows, cols);
+          store_rows(stg, zu, p.C + at + p.up, p.ld2, rows, cols);
         }
       } else {
         __nv_bfloat16* base = (o.second ? p.C2 : p.C) + row0 * p.ldc + o.n0;
@@ -611,24 +668,35 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
                         pack_bf16x2(t[6], t[7]));
     };
     if constexpr (OP == OP_GATEUP) {
-      if (p.save) {
-        __nv_bfloat16* sv = p.save + row * 2LL * p.N + o.n0 + c;
-        *reinterpret_cast<uint4*>(sv) = pack(v);
-        *reinterpret_cast<uint4*>(sv + p.N) = pack(u);
+      if (p.save_hi) {
+        const long long at = row * p.ld2 + o.n0 + c;
+        const auto keep = [&](long long x, const float (&f)[8]) {
+          *reinterpret_cast<uint4*>(p.save_hi + x) = make_uint4(swiglu::hi2(f[0], f[1]), swiglu::hi2(f[2], f[3]),
+                                                                swiglu::hi2(f[4], f[5]), swiglu::hi2(f[6], f[7]));
+          *reinterpret_cast<uint2*>(p.save_lo + x) =
+              make_uint2(swiglu::lo4(f[0], f[1], f[2], f[3]), swiglu::lo4(f[4], f[5], f[6], f[7]));
+        };
+        keep(at, v);
+        keep(at + p.up, u);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = swiglu::act(v[j], u[j]);
       *reinterpret_cast<uint4*>(p.C + row * p.ldc + o.n0 + c) = pack(v);
     } else if constexpr (OP == OP_DGRAD_ACT) {
-      const __nv_bfloat16* src = p.gateup + row * 2LL * p.N + o.n0 + c;
+      const long long at = row * p.ld2 + o.n0 + c;
       float zg[8], zu[8];
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(src), zg);
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(src + p.N), zu);
+      const auto get = [&](long long x, float (&f)[8]) {
+        const uint4 hi = *reinterpret_cast<const uint4*>(p.save_hi + x);
+        const uint2 lo = *reinterpret_cast<const uint2*>(p.save_lo + x);
+        swiglu::join4(hi.x, hi.y, lo.x, *reinterpret_cast<float(*)[4]>(&f[0]));
+        swiglu::join4(hi.z, hi.w, lo.y, *reinterpret_cast<float(*)[4]>(&f[4]));
+      };
+      get(at, zg);
+      get(at + p.up, zu);
 #pragma unroll
       for (int j = 0; j < 8; ++j) swiglu::grad(v[j], zg[j], zu[j], v[j], u[j]);
-      __nv_bfloat16* dst = p.C + row * 2LL * p.N + o.n0 + c;
-      *reinterpret_cast<uint4*>(dst) = pack(v);
-      *reinterpret_cast<uint4*>(dst + p.N) = pack(u);
+      *reinterpret_cast<uint4*>(p.C + at) = pack(v);
+      *reinterpret_cast<uint4*>(p.C + at + p.up) = pack(u);
     } else {
       *reinterpret_cast<uint4*>((o.second ? p.C2 : p.C) + row * p.ldc + o.n0 + c) = pack(v);
     }

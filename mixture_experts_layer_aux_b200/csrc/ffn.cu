@@ -51,9 +51,90 @@ static int check_cfg(const moe_ffn_config* c) {
   return MOE_OK;
 }
 
+static int cdiv(int a, int b) { return (a + b - 1) / b; }
+static int pad64(int n) { return (n + 63) / 64 * 64; }
+
+// A row-major bf16 operand: rows of ld elements.
+struct Mat {
+  const void* p;
+  long long ld;
+};
+
+// Rows that do not start on 128 bytes cost the tensor-core kernels a quarter of their rate or more (every 128-byte row
+// of a TMA box is on two lines; T = 4001, H = 4104, F = 8200, a training step: 920 TFLOP/s, and 1206 at H = 4096,
+// F = 8192). Buffers of this file are therefore padded to 64 elements, and with enough tokens the caller's ragged
+// operands are copied to padded ones first, once per call.
+constexpr int PAD_T_FWD = 1024, PAD_T_BWD = 512;
+static bool pads(const moe_ffn_config* c, bool bwd) {
+  return c->T >= (bwd ? PAD_T_BWD : PAD_T_FWD) && (c->H % 64 != 0 || c->F % 64 != 0);
+}
+
+// The caller's operands [rows, n] as padded copies.
+struct Padded {
+  __nv_bfloat16 *x, *dY, *Wg, *Wu, *Wd;
+};
+static Padded carve_padded(Carve& cv, const moe_ffn_config* c, bool bwd) {
+  Padded q{};
+  if (!pads(c, bwd)) return q;
+  const size_t T = c->T, Hp = pad64(c->H), Fp = pad64(c->F);
+  if (c->H % 64 != 0) {
+    q.x = cv.take<__nv_bfloat16>(T * Hp);
+    if (bwd) q.dY = cv.take<__nv_bfloat16>(T * Hp);
+    q.Wg = cv.take<__nv_bfloat16>((size_t)c->F * Hp);
+    q.Wu = cv.take<__nv_bfloat16>((size_t)c->F * Hp);
+  }
+  if (c->F % 64 != 0) q.Wd = cv.take<__nv_bfloat16>((size_t)c->H * Fp);
+  return q;
+}
+
+struct PadJobs {
+  struct {
+    const uint4* src;
+    uint4* dst;
+    int rows, n8, ld8;  // rows of n8 vectors of 8 elements, ld8 apart at dst
+  } job[5];
+};
+// grid.y: job. The columns past n are not written: no kernel reads them.
+__global__ void __launch_bounds__(256) pad_kernel(const PadJobs j) {
+  griddep_launch_dependents();
+  const auto& b = j.job[blockIdx.y];
+  const long long n = (long long)b.rows * b.n8, step = (long long)gridDim.x * 256;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += 4 * step) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * step < n) v[k] = __ldcs(b.src + i + k * step);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const long long e = i + k * step;
+      if (e < n) b.dst[e / b.n8 * b.ld8 + e % b.n8] = v[k];
+    }
+  }
+}
+
+// Replaces m by its padded copy, where there is one.
+static void add_job(PadJobs& j, int& n, Mat& m, __nv_bfloat16* dst, int rows, int cols) {
+  if (!dst || !m.p) return;
+  const int ld = pad64(cols);
+  j.job[n].src = static_cast<const uint4*>(m.p);
+  j.job[n].dst = reinterpret_cast<uint4*>(dst);
+  j.job[n].rows = rows;
+  j.job[n].n8 = cols / 8;
+  j.job[n].ld8 = ld / 8;
+  ++n;
+  m = Mat{dst, ld};
+}
+static int run_jobs(const PadJobs& j, int n, cudaStream_t st) {
+  if (n == 0) return MOE_OK;
+  pad_kernel<<<dim3(4 * moe_host::num_sms(), n), 256, 0, st>>>(j);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
 struct FwdWs {
-  __nv_bfloat16* a;
+  __nv_bfloat16* a;  // [T, Fp]
   float* part;
+  Padded pad;
   uint8_t *xq, *xq_sf, *aq, *aq_sf;
   int32_t* off;
 };
@@ -68,45 +149,51 @@ static size_t carve_fwd(void* ws, const moe_ffn_config* c, FwdWs* w) {
     w->aq_sf = cv.take<uint8_t>(T * F / 32);
     w->off = cv.take<int32_t>(2);
   } else {
-    if (!c->save_for_bwd) w->a = cv.take<__nv_bfloat16>(T * F);
+    if (!c->save_for_bwd) w->a = cv.take<__nv_bfloat16>(T * pad64(c->F));
     if (c->T > STREAM_T) w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
+    w->pad = carve_padded(cv, c, false);
   }
   return cv.used;
 }
 
+// What the backward reads: the pre-activations (24 bits, swiglu.cuh; gate in columns [0, F), up in [Fp, Fp + F) of
+// rows of 2 Fp) and the activation.
 struct Saved {
-  __nv_bfloat16* gateup;  // [T, 2F]: gate in columns [0, F), up in [F, 2F)
-  __nv_bfloat16* a;       // [T, F]
+  __nv_bfloat16* hi;  // [T, 2 Fp]
+  uint8_t* lo;        // [T, 2 Fp]
+  __nv_bfloat16* a;   // [T, Fp]
 };
 static size_t carve_saved(void* p, const moe_ffn_config* c, Saved* s) {
   Carve cv(p);
-  s->gateup = cv.take<__nv_bfloat16>((size_t)c->T * 2 * c->F);
-  s->a = cv.take<__nv_bfloat16>((size_t)c->T * c->F);
+  const size_t n = (size_t)c->T * pad64(c->F);
+  s->hi = cv.take<__nv_bfloat16>(2 * n);
+  s->lo = cv.take<uint8_t>(2 * n);
+  s->a = cv.take<__nv_bfloat16>(n);
   return cv.used;
 }
 
 struct BwdWs {
-  __nv_bfloat16* dgu;  // [T, 2F]: dgate | dup
+  __nv_bfloat16* dgu;  // [T, 2 Fp]: dgate | dup
   float* part;
+  Padded pad;
 };
 static size_t carve_bwd(void* ws, const moe_ffn_config* c, BwdWs* w) {
   Carve cv(ws);
-  w->dgu = cv.take<__nv_bfloat16>((size_t)c->T * 2 * c->F);
+  w->dgu = cv.take<__nv_bfloat16>((size_t)c->T * 2 * pad64(c->F));
   w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
+  w->pad = carve_padded(cv, c, true);
   return cv.used;
 }
 
-// bf16 [outer, inner] with a row stride of ld elements, boxes of 64 x box_outer.
-static bool tmap(CUtensorMap* m, const void* base, long long inner, long long outer, long long ld, int box_outer) {
-  return moe_host::encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, (uint64_t)ld * 2, 64,
+// bf16 [outer, inner], boxes of 64 x box_outer.
+static bool tmap(CUtensorMap* m, Mat a, long long inner, long long outer, int box_outer) {
+  return moe_host::encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.p, inner, outer, (uint64_t)a.ld * 2, 64,
                                   box_outer);
 }
-static int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-// H, F: the block's sizes (every operand's row length).
-static Params base_params(int H, int F, int M, int N, int KB, float* part, void* C, long long ldc) {
+static Params base_params(int M, int N, int KB, Mat A, Mat B, float* part, void* C, long long ldc) {
   Params p{};
-  p.ragged = H % 64 != 0 || F % 64 != 0;
+  p.ragged = A.ld % 64 != 0 || B.ld % 64 != 0;
   p.M = M;
   p.N = N;
   p.KB = KB;
@@ -118,70 +205,82 @@ static Params base_params(int H, int F, int M, int N, int KB, float* part, void*
   return p;
 }
 
-static int gateup(int T, int H, int F, const void* x, const void* Wg, const void* Wu, void* a, void* save, float* part,
+static int gateup(int T, int H, int F, Mat x, Mat Wg, Mat Wu, __nv_bfloat16* a, const Saved& s, float* part,
                   cudaStream_t st, bool dep) {
-  Params p = base_params(H, F, T, F, cdiv(H, dense::BK), part, a, F);
-  if (!tmap(&p.tmA, x, H, T, H, 128) || !tmap(&p.tmB0, Wg, H, F, H, 128) || !tmap(&p.tmB1, Wu, H, F, H, 128))
+  Params p = base_params(T, F, cdiv(H, dense::BK), x, Wg, part, a, pad64(F));
+  if (!tmap(&p.tmA, x, H, T, 128) || !tmap(&p.tmB0, Wg, H, F, 128) || !tmap(&p.tmB1, Wu, H, F, 128))
     return MOE_ERR_CUDA;
-  p.save = static_cast<__nv_bfloat16*>(save);
+  p.save_hi = s.hi;
+  p.save_lo = s.lo;
+  p.ld2 = 2LL * pad64(F);
+  p.up = pad64(F);
   return dense::launch<dense::OP_GATEUP>(p, st, dep);
 }
 
-static int down(int T, int H, int F, const void* a, const void* Wd, void* y, float* part, cudaStream_t st, bool dep) {
-  Params p = base_params(H, F, T, H, cdiv(F, dense::BK), part, y, H);
-  if (!tmap(&p.tmA, a, F, T, F, 128) || !tmap(&p.tmB0, Wd, F, H, F, 128)) return MOE_ERR_CUDA;
+static int down(int T, int H, int F, const __nv_bfloat16* a, Mat Wd, void* y, float* part, cudaStream_t st, bool dep) {
+  const Mat am{a, pad64(F)};
+  Params p = base_params(T, H, cdiv(F, dense::BK), am, Wd, part, y, H);
+  if (!tmap(&p.tmA, am, F, T, 128) || !tmap(&p.tmB0, Wd, F, H, 128)) return MOE_ERR_CUDA;
   return dense::launch<dense::OP_DOWN>(p, st, dep);
 }
 
-static int dgrad_act(int T, int H, int F, const void* dY, const void* Wd, const void* gateup, void* dgu, float* part,
+static int dgrad_act(int T, int H, int F, Mat dY, Mat Wd, const Saved& s, __nv_bfloat16* dgu, float* part,
                      cudaStream_t st, bool dep) {
-  Params p = base_params(H, F, T, F, cdiv(H, dense::BK), part, dgu, 2LL * F);
-  if (!tmap(&p.tmA, dY, H, T, H, 128) || !tmap(&p.tmB0, Wd, F, H, F, 64)) return MOE_ERR_CUDA;
-  p.gateup = static_cast<const __nv_bfloat16*>(gateup);
+  Params p = base_params(T, F, cdiv(H, dense::BK), dY, Wd, part, dgu, 0);
+  if (!tmap(&p.tmA, dY, H, T, 128) || !tmap(&p.tmB0, Wd, F, H, 64)) return MOE_ERR_CUDA;
+  p.save_hi = s.hi;
+  p.save_lo = s.lo;
+  p.ld2 = 2LL * pad64(F);
+  p.up = pad64(F);
   return dense::launch<dense::OP_DGRAD_ACT>(p, st, dep);
 }
 
-static int dgrad_x(int T, int H, int F, const __nv_bfloat16* dgu, const void* Wg, const void* Wu, void* dX,
-                   float* part, cudaStream_t st, bool dep) {
+static int dgrad_x(int T, int H, int F, const __nv_bfloat16* dgu, Mat Wg, Mat Wu, void* dX, float* part,
+                   cudaStream_t st, bool dep) {
   const int kb = cdiv(F, dense::BK);
-  Params p = base_params(H, F, T, H, 2 * kb, part, dX, H);
+  const Mat dg{dgu, 2LL * pad64(F)}, du{dgu + pad64(F), 2LL * pad64(F)};
+  Params p = base_params(T, H, 2 * kb, dg, Wg, part, dX, H);
   p.kb_split = kb;
-  if (!tmap(&p.tmA, dgu, F, T, 2LL * F, 128) || !tmap(&p.tmA2, dgu + F, F, T, 2LL * F, 128) ||
-      !tmap(&p.tmB0, Wg, H, F, H, 64) || !tmap(&p.tmB1, Wu, H, F, H, 64))
+  if (!tmap(&p.tmA, dg, F, T, 128) || !tmap(&p.tmA2, du, F, T, 128) || !tmap(&p.tmB0, Wg, H, F, 64) ||
+      !tmap(&p.tmB1, Wu, H, F, 64))
     return MOE_ERR_CUDA;
   return dense::launch<dense::OP_DGRAD_X>(p, st, dep);
 }
 
 // dW [M, N] = sum_t dO[t, :M]^T act[t, :N]; with dO2, a second [M, N] from it into dW2 in the same launch.
-static int wgrad(int T, int M, int N, const void* dO, const void* dO2, long long ld_dO, const void* act, void* dW,
-                 void* dW2, float* part, cudaStream_t st, bool dep) {
-  Params p = base_params(M, N, M, N, cdiv(T, dense::BK), part, dW, N);
-  if (!tmap(&p.tmA, dO, M, T, ld_dO, 64) || !tmap(&p.tmB0, act, N, T, N, 64)) return MOE_ERR_CUDA;
-  if (dO2) {
-    if (!tmap(&p.tmA2, dO2, M, T, ld_dO, 64)) return MOE_ERR_CUDA;
+static int wgrad(int T, int M, int N, Mat dO, Mat dO2, Mat act, void* dW, void* dW2, float* part, cudaStream_t st,
+                 bool dep) {
+  Params p = base_params(M, N, cdiv(T, dense::BK), dO, act, part, dW, N);
+  if (!tmap(&p.tmA, dO, M, T, 64) || !tmap(&p.tmB0, act, N, T, 64)) return MOE_ERR_CUDA;
+  if (dO2.p) {
+    if (!tmap(&p.tmA2, dO2, M, T, 64)) return MOE_ERR_CUDA;
     p.halves = 2;
     p.C2 = static_cast<__nv_bfloat16*>(dW2);
   }
   return dense::launch<dense::OP_WGRAD>(p, st, dep);
 }
 
-// One product of the streaming path: W1 for gate/up, scales for MXFP8.
+// One product of the streaming path: W1 for gate/up, scales for MXFP8; x has rows of ldx elements, out of ldo.
 template <bool MX, bool GATEUP>
 static int stream_gemm(int T, int N, int K, const void* W0, const void* W1, const uint8_t* sf0, const uint8_t* sf1,
-                       const void* x, const uint8_t* x_sf, void* out, uint8_t* out_sf, void* save, cudaStream_t st,
-                       bool dep, const void* W_next = nullptr) {
+                       Mat x, const uint8_t* x_sf, void* out, long long ldo, uint8_t* out_sf, const Saved& s,
+                       cudaStream_t st, bool dep, const void* W_next = nullptr) {
   stream::Params p = stream::plan<MX, GATEUP>(T, N, K);
   if (GATEUP && !stream::plan_next<MX>(p, W_next)) return MOE_ERR_CUDA;
-  if (!stream::encode_maps<MX>(&p.tmW0, &p.tmW0t, p, W0, N, p.r) ||
-      (GATEUP && !stream::encode_maps<MX>(&p.tmW1, &p.tmW1t, p, W1, N, p.r)) ||
-      !stream::encode_maps<MX>(&p.tmX, &p.tmXt, p, x, T, T))
+  if (!stream::encode_maps<MX>(&p.tmW0, &p.tmW0t, p, W0, N, p.r, K) ||
+      (GATEUP && !stream::encode_maps<MX>(&p.tmW1, &p.tmW1t, p, W1, N, p.r, K)) ||
+      !stream::encode_maps<MX>(&p.tmX, &p.tmXt, p, x.p, T, T, x.ld))
     return MOE_ERR_CUDA;
   p.sf0 = sf0;
   p.sf1 = sf1;
   p.x_sf = x_sf;
   p.out = out;
+  p.ldo = ldo;
   p.out_sf = out_sf;
-  p.save = static_cast<__nv_bfloat16*>(save);
+  p.save_hi = reinterpret_cast<uint16_t*>(s.hi);
+  p.save_lo = s.lo;
+  p.ld2 = 2LL * pad64(N);
+  p.up = pad64(N);
   return stream::launch<MX, GATEUP>(p, st, dep);
 }
 
@@ -215,16 +314,24 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __nv_bfloat16* __re
 }
 
 static int fwd_bf16(const moe_ffn_config* c, const void* x, const void* Wg, const void* Wu, const void* Wd, void* y,
-                    __nv_bfloat16* a, __nv_bfloat16* save, float* part, cudaStream_t st) {
-  const int T = c->T, H = c->H, F = c->F;
+                    __nv_bfloat16* a, const Saved& s, const FwdWs& w, cudaStream_t st) {
+  const int T = c->T, H = c->H, F = c->F, Fp = pad64(F);
   if (T <= STREAM_T) {
-    FFN_RC((stream_gemm<false, true>(T, F, H, Wg, Wu, nullptr, nullptr, x, nullptr, a, nullptr, save, st, false,
-                                     Wd)));
-    return stream_gemm<false, false>(T, H, F, Wd, nullptr, nullptr, nullptr, a, nullptr, y, nullptr, nullptr, st,
-                                     true);
+    FFN_RC((stream_gemm<false, true>(T, F, H, Wg, Wu, nullptr, nullptr, Mat{x, H}, nullptr, a, Fp, nullptr, s, st,
+                                     false, Wd)));
+    return stream_gemm<false, false>(T, H, F, Wd, nullptr, nullptr, nullptr, Mat{a, Fp}, nullptr, y, H, nullptr,
+                                     Saved{}, st, true);
   }
-  FFN_RC(gateup(T, H, F, x, Wg, Wu, a, save, part, st, false));
-  return down(T, H, F, a, Wd, y, part, st, true);
+  Mat mx{x, H}, mg{Wg, H}, mu{Wu, H}, md{Wd, F};
+  PadJobs j;
+  int n = 0;
+  add_job(j, n, mx, w.pad.x, T, H);
+  add_job(j, n, mg, w.pad.Wg, F, H);
+  add_job(j, n, mu, w.pad.Wu, F, H);
+  add_job(j, n, md, w.pad.Wd, H, F);
+  FFN_RC(run_jobs(j, n, st));
+  FFN_RC(gateup(T, H, F, mx, mg, mu, a, s, w.part, st, n > 0));
+  return down(T, H, F, a, md, y, w.part, st, true);
 }
 
 static int fwd_mxfp8(const moe_ffn_config* c, const void* x, const uint8_t* x_sf, const void* Wg, const void* Wu,
@@ -245,10 +352,10 @@ static int fwd_mxfp8(const moe_ffn_config* c, const void* x, const uint8_t* x_sf
     x_sf = w.xq_sf;
   }
   if (T <= STREAM_T) {
-    FFN_RC((stream_gemm<true, true>(T, F, H, Wg, Wu, Wg_sf, Wu_sf, x, x_sf, w.aq, w.aq_sf, nullptr, st, quant,
-                                    Wd)));
-    return stream_gemm<true, false>(T, H, F, Wd, nullptr, Wd_sf, nullptr, w.aq, w.aq_sf, y, nullptr, nullptr, st,
-                                    true);
+    FFN_RC((stream_gemm<true, true>(T, F, H, Wg, Wu, Wg_sf, Wu_sf, Mat{x, H}, x_sf, w.aq, F, w.aq_sf, Saved{}, st,
+                                    quant, Wd)));
+    return stream_gemm<true, false>(T, H, F, Wd, nullptr, Wd_sf, nullptr, Mat{w.aq, F}, w.aq_sf, y, H, nullptr,
+                                    Saved{}, st, true);
   }
   FFN_RC(moe_impl::fill_offsets2(w.off, T, st));
   FFN_RC(moe_impl::gemm_gateup_mx(T, 1, H, F, x, x_sf, Wg, Wg_sf, Wu, Wu_sf, w.off, nullptr, w.aq, w.aq_sf, nullptr,
@@ -296,7 +403,7 @@ extern "C" int moe_ffn_fwd(const moe_ffn_config* cfg, const void* x, const uint8
   if (mx) return fwd_mxfp8(cfg, x, x_sf, W_g, W_u, W_d, W_g_sf, W_u_sf, W_d_sf, y, w, st);
   Saved s{};
   if (saved) carve_saved(saved, cfg, &s);
-  return fwd_bf16(cfg, x, W_g, W_u, W_d, y, saved ? s.a : w.a, s.gateup, w.part, st);
+  return fwd_bf16(cfg, x, W_g, W_u, W_d, y, saved ? s.a : w.a, s, w, st);
 }
 
 extern "C" int moe_ffn_bwd(const moe_ffn_config* cfg, const void* dY, const void* x, const void* W_g, const void* W_u,
@@ -318,16 +425,28 @@ extern "C" int moe_ffn_bwd(const moe_ffn_config* cfg, const void* dY, const void
   carve_saved(const_cast<void*>(saved), cfg, &s);
   const int T = cfg->T, H = cfg->H, F = cfg->F;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  bool dep = false;
+  const int Fp = pad64(F);
+  Mat mdy{dY, H}, mx{dW_g ? x : nullptr, H}, mg{dX ? W_g : nullptr, H}, mu{dX ? W_u : nullptr, H},
+      md{dX || dW_g ? W_d : nullptr, F};
+  PadJobs j;
+  int n = 0;
+  add_job(j, n, mdy, w.pad.dY, T, H);
+  add_job(j, n, mx, w.pad.x, T, H);
+  add_job(j, n, mg, w.pad.Wg, F, H);
+  add_job(j, n, mu, w.pad.Wu, F, H);
+  add_job(j, n, md, w.pad.Wd, H, F);
+  FFN_RC(run_jobs(j, n, st));
+  bool dep = n > 0;
   if (dX || dW_g) {
-    FFN_RC(dgrad_act(T, H, F, dY, W_d, s.gateup, w.dgu, w.part, st, dep));
+    FFN_RC(dgrad_act(T, H, F, mdy, md, s, w.dgu, w.part, st, dep));
     dep = true;
   }
   if (dW_d) {
-    FFN_RC(wgrad(T, H, F, dY, nullptr, H, s.a, dW_d, nullptr, w.part, st, dep));
+    FFN_RC(wgrad(T, H, F, mdy, Mat{}, Mat{s.a, Fp}, dW_d, nullptr, w.part, st, dep));
     dep = true;
   }
-  if (dX) FFN_RC(dgrad_x(T, H, F, w.dgu, W_g, W_u, dX, w.part, st, dep));
-  if (dW_g) FFN_RC(wgrad(T, F, H, w.dgu, w.dgu + F, 2LL * F, x, dW_g, dW_u, w.part, st, true));
+  if (dX) FFN_RC(dgrad_x(T, H, F, w.dgu, mg, mu, dX, w.part, st, dep));
+  if (dW_g)
+    FFN_RC(wgrad(T, F, H, Mat{w.dgu, 2LL * Fp}, Mat{w.dgu + Fp, 2LL * Fp}, mx, dW_g, dW_u, w.part, st, true));
   return MOE_OK;
 }

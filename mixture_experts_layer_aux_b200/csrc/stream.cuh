@@ -88,9 +88,13 @@ struct __align__(64) Params {
   int next_r, next_s, next_tiles;   // the stages to bring into L2 (from, to)
   int next_from, next_to;
   const uint8_t *sf0, *sf1, *x_sf;  // MXFP8 scales, [rows, K/32]
-  void* out;                        // gate/up: [T, N] bf16, or e4m3 codes; down: [T, N] bf16
+  void* out;                        // gate/up: bf16 or e4m3 codes; down: bf16; rows of ldo elements
+  long long ldo;
   uint8_t* out_sf;                  // MXFP8 gate/up: [T, N/32]
-  __nv_bfloat16* save;              // bf16 gate/up: gate | up [T, 2N], or NULL
+  uint16_t* save_hi;                // bf16 gate/up: pre-activations (swiglu.cuh), rows of ld2, up from column `up`; or
+  uint8_t* save_lo;                 // NULL
+  long long ld2;
+  int up;
   int T, N, K;                      // tokens, weight rows, reduction length
   int r, s;                         // weight rows per tile, K blocks per stage
   int KB, KS;                       // K blocks (128 bytes), stages of s blocks
@@ -180,6 +184,14 @@ MOE_DEV uint8_t quant_lane(float a, uint8_t& sb) {
   const float am = fmaxf(fabsf(a), 0.f);
   sb = ggmx::mx_scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(am))));
   return __nv_cvt_float_to_fp8(a * ggmx::mx_inv_scale(sb), __NV_SATFINITE, __NV_E4M3);
+}
+
+MOE_DEV void save_preact(const Params& p, int tok, int col, float g, float u) {
+  const long long at = tok * p.ld2 + col;
+  p.save_hi[at] = (uint16_t)(__float_as_uint(g) >> 16);
+  p.save_lo[at] = (uint8_t)(__float_as_uint(g) >> 8);
+  p.save_hi[at + p.up] = (uint16_t)(__float_as_uint(u) >> 16);
+  p.save_lo[at + p.up] = (uint8_t)(__float_as_uint(u) >> 8);
 }
 
 template <bool MX, bool GATEUP>
@@ -565,7 +577,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           if (c + i >= p.T) break;
-          const long long o = (long long)(c + i) * p.N + n0 + row;
+          const long long o = (c + i) * p.ldo + n0 + row;
           if constexpr (GATEUP) {
             const float a = swiglu::act(v[i], u[i]);
             if (MX) {
@@ -577,11 +589,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
               }
             } else if (ok) {
               static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a);
-              if (p.save) {
-                __nv_bfloat16* sv = p.save + (long long)(c + i) * 2 * p.N + n0 + row;
-                sv[0] = __float2bfloat16_rn(v[i]);
-                sv[p.N] = __float2bfloat16_rn(u[i]);
-              }
+              if (p.save_hi) save_preact(p, c + i, n0 + row, v[i], u[i]);
             }
           } else if (ok) {
             static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v[i]);
@@ -688,7 +696,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
           if (GATEUP) u += pt[up_tail];
         }
         const float a = GATEUP ? swiglu::act(g, u) : g;
-        const long long tok = (tl << lc) + rank, o = tok * p.N + n0 + f;
+        const int tok = (tl << lc) + rank;
+        const long long o = tok * p.ldo + n0 + f;
         if (MX && GATEUP) {
           uint8_t sb;
           const uint8_t code = quant_lane(ok ? a : 0.f, sb);
@@ -698,11 +707,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
           }
         } else if (ok) {
           static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a);
-          if (GATEUP && p.save) {
-            __nv_bfloat16* sv = p.save + tok * 2 * p.N + n0 + f;
-            sv[0] = __float2bfloat16_rn(g);
-            sv[p.N] = __float2bfloat16_rn(u);
-          }
+          if (GATEUP && p.save_hi) save_preact(p, tok, n0 + f, g, u);
         }
       }
     }
@@ -801,20 +806,20 @@ Params plan(int T, int N, int K) {
   return p;
 }
 
-// Tensor map of a row-major [rows, K] operand: boxes of 128 bytes x box rows x s blocks of K.
+// Tensor map of a [rows, K] operand with rows of ld elements: boxes of 128 bytes x box rows x s blocks of K.
 template <bool MX>
-bool encode_map(CUtensorMap* m, const Params& p, const void* base, int rows, int box) {
+bool encode_map(CUtensorMap* m, const Params& p, const void* base, int rows, int box, long long ld) {
   const uint64_t eb = MX ? 1 : 2, step = MX ? 128 : 64;
   return moe_host::encode_tmap_3d(m, MX ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
-                                  p.z ? step : (uint64_t)p.K, rows, p.z ? p.KB : 1, p.K * eb, ROW_BYTES, step, box,
+                                  p.z ? step : (uint64_t)p.K, rows, p.z ? p.KB : 1, ld * eb, ROW_BYTES, step, box,
                                   p.s);
 }
 
 // The maps of one operand: the whole blocks, and the tail.
 template <bool MX>
-bool encode_maps(CUtensorMap* m, CUtensorMap* mt, const Params& p, const void* base, int rows, int box) {
-  if (!encode_map<MX>(m, p, base, rows, box)) return false;
-  return !p.tail || moe_host::encode_tmap_2d(mt, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, p.K, rows, (uint64_t)p.K * 2,
+bool encode_maps(CUtensorMap* m, CUtensorMap* mt, const Params& p, const void* base, int rows, int box, long long ld) {
+  if (!encode_map<MX>(m, p, base, rows, box, ld)) return false;
+  return !p.tail || moe_host::encode_tmap_2d(mt, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, p.K, rows, (uint64_t)ld * 2,
                                              64, box);
 }
 
@@ -831,7 +836,7 @@ bool plan_next(Params& p, const void* W_next) {
   p.next_from = d.stages;
   const long long n = d.stages + NEXT_BYTES / ((long long)d.tiles * d.s * d.r * ROW_BYTES);
   p.next_to = (int)(n < d.KS ? n : d.KS);
-  return encode_map<MX>(&p.tmNext, d, W_next, d.N, d.r);
+  return encode_map<MX>(&p.tmNext, d, W_next, d.N, d.r, d.K);
 }
 
 // dep: the kernel before it in the stream is one of the same call's (the weights are not its results).
