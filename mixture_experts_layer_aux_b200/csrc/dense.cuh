@@ -7,16 +7,15 @@
 // Everything past an edge of M, N or K is zero-filled by TMA on the way in and
 // predicated on the way out, so no operand is padded.
 //
-// Two forms (template CG):
-//   1  a CTA computes 128 x 256 (tcgen05 M128 N256 K16), four 48 KB stages;
-//   2  a pair of CTAs on neighbouring SMs computes 256 x 256 with
-//      cta_group::2: each holds its 128 rows of A and half of B's 256 rows, so
-//      a stage is 32 KB per SM, six fit, and every SM moves a third less
-//      through L2 and shared memory per product. Taken where rounding M up to
-//      256 costs little.
+// Four forms. Template CG:
+//   1  a CTA computes 128 x BN (tcgen05 M128 K16);
+//   2  a pair of CTAs on neighbouring SMs computes 256 x BN with cta_group::2:
+//      each holds its 128 rows of A and half of B's, so every SM moves less
+//      through L2 and shared memory per product.
+// Template BN: 256, or 128 where that fills the SMs better. plan() chooses.
 // Roles (320 threads, one CTA per SM, persistent), as in the grouped GEMM of
 // gemm.cuh: warp 0 TMA producer, warp 1 MMA issuer (the pair's first CTA) and
-// TMEM owner (two 256-column accumulators), warps 2..9 epilogue (lane quadrant
+// TMEM owner (two BN-column accumulators), warps 2..9 epilogue (lane quadrant
 // w % 4, column half). Every wait is bounded (MOE_WAIT_NS).
 //
 // Work split. Whole tiles go round robin over the CTAs (pairs) while they fill
@@ -30,20 +29,20 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "elect.cuh"
 #include "swiglu.cuh"
 
 namespace dense {
 
-constexpr int BM = 128, BN = 256, BK = 64;
+constexpr int BM = 128, BK = 64, MAX_BN = 256;
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int EPI_WARPS = 8;
 constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
-constexpr int TMEM_COLS = 2 * BN;
 constexpr int STG_ROW = 80;  // staging: 32 rows x (64 + 16) bytes per epilogue warp
 constexpr int STG_BYTES = EPI_WARPS * 32 * STG_ROW;
 constexpr int BAR_BYTES = 256;
 constexpr int MAX_CTAS = 160;                            // CTAs of one launch (one per SM)
-constexpr size_t SLOT_FLOATS = (size_t)BM * BN;          // one CTA's partial accumulator
+constexpr size_t SLOT_FLOATS = (size_t)BM * MAX_BN;          // one CTA's partial accumulator
 constexpr size_t PART_BYTES = 2ull * MAX_CTAS * SLOT_FLOATS * sizeof(float);
 
 enum Op : int {
@@ -59,7 +58,6 @@ struct __align__(64) Params {
   int M, N;            // output rows and columns (per half when m_split)
   int KB;              // k-blocks of 64
   int kb_split;        // OP_DGRAD_X: k-blocks of the first half
-  int ragged;          // an operand's rows do not start on 128 bytes
   int halves;          // OP_WGRAD: 2 for two stacked outputs of M rows each (A2, C2 the second), else 1
   int tiles_m, tiles_n;
   int tm_split;        // m-tiles of one half
@@ -116,15 +114,17 @@ struct Walk {
   }
 };
 
-template <int OP, int CG>
+template <int OP, int CG, int BN_>
 struct Cfg {
+  static constexpr int BN = BN_;
   static constexpr bool A_MN = OP == OP_WGRAD;
   static constexpr bool B_MN = OP >= OP_DGRAD_ACT;
   static constexpr int N_STEP = OP == OP_GATEUP ? BN / 2 : BN;  // output columns per tile
   static constexpr int B_ROWS = BN / CG;                        // of B, per CTA
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK * 2;
-  static constexpr int kStages = CG == 2 ? 6 : 4;
+  static constexpr int kStages = BN == 128 ? (CG == 2 ? 8 : 6) : CG == 2 ? 6 : 4;
   static constexpr int SMEM_BYTES = 1024 + kStages * STAGE_BYTES + BAR_BYTES + STG_BYTES;
+  static constexpr int B_BOX = OP == OP_GATEUP ? BN / 2 : B_ROWS < 128 ? B_ROWS : 128;  // rows of a K-major B box
   static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
@@ -133,16 +133,16 @@ struct Origin {
   bool second;             // OP_WGRAD: the second half
 };
 // rank: the CTA's place in its pair.
-template <int OP, int CG>
+template <int OP, int CG, int BN>
 MOE_DEV Origin origin(const Params& p, int tile, int rank) {
   Origin o;
   const int mt = tile % p.tiles_m;  // m fastest: the CTAs of a wave share a few column panels of B
   const int nt = tile / p.tiles_m;
   o.second = OP == OP_WGRAD && mt >= p.tm_split;
   o.m0 = (mt - (o.second ? p.tm_split : 0)) * BM * CG + rank * BM;
-  o.n0 = nt * Cfg<OP, CG>::N_STEP;
+  o.n0 = nt * Cfg<OP, CG, BN>::N_STEP;
   o.rows = min(BM, p.M - o.m0);
-  o.cols = min(Cfg<OP, CG>::N_STEP, p.N - o.n0);
+  o.cols = min(Cfg<OP, CG, BN>::N_STEP, p.N - o.n0);
   return o;
 }
 
@@ -204,23 +204,23 @@ MOE_DEV void arrive_first(uint64_t* bar) {
                  : "memory");
 }
 template <int CG>
-MOE_DEV void alloc_tmem(uint32_t* slot) {
+MOE_DEV void alloc_tmem(uint32_t* slot, uint32_t cols) {
   if constexpr (CG == 1) {
-    tmem_alloc(slot, TMEM_COLS);
+    tmem_alloc(slot, cols);
     tmem_relinquish();
   } else {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
-                 "r"(TMEM_COLS)
+                 "r"(cols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
 }
 template <int CG>
-MOE_DEV void free_tmem(uint32_t taddr) {
+MOE_DEV void free_tmem(uint32_t taddr, uint32_t cols) {
   if constexpr (CG == 1)
-    tmem_dealloc(taddr, TMEM_COLS);
+    tmem_dealloc(taddr, cols);
   else
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(TMEM_COLS) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
 }
 
 // 32 bf16 of each of the warp's 32 rows (16 words per lane, lane = row) to dst (row-contiguous through the
@@ -322,9 +322,9 @@ MOE_DEV void pack32(const float (&v)[32], uint32_t (&w)[16]) {
   for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
 }
 
-template <int OP, int CG>
+template <int OP, int CG, int BN>
 __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<OP, CG>;
+  using C = Cfg<OP, CG, BN>;
   constexpr int kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
     tma_prefetch_desc(&p.tmA);
     tma_prefetch_desc(&p.tmB0);
   }
-  if (warp == 1) alloc_tmem<CG>(tmem_slot);
+  if (warp == 1) alloc_tmem<CG>(tmem_slot, 2 * BN);
   __syncthreads();
   if (CG == 2) pair_sync();  // both CTAs' barriers exist before either signals the other
   tc_fence_after();
@@ -369,20 +369,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
   Walk walk(p, (int)blockIdx.x / CG, (int)gridDim.x / CG);
   if (warp == 0) {
     // ======================= TMA producer: this CTA's rows of A and B
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued_mask = 0, issued_par = 0;
-      for (Seg s = walk.next(p); s.tile >= 0 && !aborted; s = walk.next(p)) {
-        const Origin o = origin<OP, CG>(p, s.tile, rank);
-        const int b0 = o.n0 + (OP == OP_GATEUP ? 0 : rank * C::B_ROWS);
-        for (int kb = s.kb0; kb < s.kb0 + s.nkb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) {
-            aborted = true;
-            break;
-          }
+    int stage = 0;
+    uint32_t phase = 0, issued_mask = 0, issued_par = 0;
+    for (Seg s = walk.next(p); s.tile >= 0 && !aborted; s = walk.next(p)) {
+      const Origin o = origin<OP, CG, BN>(p, s.tile, rank);
+      const int b0 = o.n0 + (OP == OP_GATEUP ? 0 : rank * C::B_ROWS);
+      for (int kb = s.kb0; kb < s.kb0 + s.nkb; ++kb) {
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) {
+          aborted = true;
+          break;
+        }
+        issued_mask |= 1u << stage;
+        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * C::STAGE_BYTES);
-          issued_mask |= 1u << stage;
-          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
           uint8_t* sA = smem + stage * C::STAGE_BYTES;
           uint8_t* sB = sA + A_BYTES;
           uint64_t* bar = &full[stage];
@@ -396,90 +396,93 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
             load_tile<CG>(sA + 64 * BK * 2, mA, o.m0 + 64, kc, bar);
           }
           if constexpr (OP == OP_GATEUP) {
-            // columns 0..127 of the accumulator are gate, 128..255 up
+            // the first half of the accumulator's columns is gate, the second up
             if constexpr (CG == 2) {
               load_tile<CG>(sB, rank ? &p.tmB1 : &p.tmB0, kc, b0, bar);
             } else {
               load_tile<CG>(sB, &p.tmB0, kc, b0, bar);
-              load_tile<CG>(sB + 128 * BK * 2, &p.tmB1, kc, b0, bar);
+              load_tile<CG>(sB + BN / 2 * BK * 2, &p.tmB1, kc, b0, bar);
             }
           } else if constexpr (!C::B_MN) {
 #pragma unroll
-            for (int j = 0; j < C::B_ROWS / 128; ++j)
-              load_tile<CG>(sB + j * 128 * BK * 2, &p.tmB0, kc, b0 + 128 * j, bar);
+            for (int j = 0; j < C::B_ROWS / C::B_BOX; ++j)
+              load_tile<CG>(sB + j * C::B_BOX * BK * 2, &p.tmB0, kc, b0 + C::B_BOX * j, bar);
           } else {
             const CUtensorMap* mB = hi ? &p.tmB1 : &p.tmB0;
 #pragma unroll
             for (int j = 0; j < C::B_ROWS / 64; ++j) load_tile<CG>(sB + j * 64 * BK * 2, mB, b0 + 64 * j, kc, bar);
           }
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+        }
+        __syncwarp();
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      if (CG == 2) {
-        // no commit of the first CTA may arrive here after this CTA has left: wait until every stage is released
-        for (int i = 0; i < kStages && !aborted; ++i) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) aborted = true;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+    }
+    if (CG == 2) {
+      // no commit of the first CTA may arrive here after this CTA has left: wait until every stage is released
+      for (int i = 0; i < kStages && !aborted; ++i) {
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) aborted = true;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      if (*abort_flag) {
-        // every TMA this thread issued must land before the CTA exits (a pair's second CTA cannot see its own land:
-        // it gives them a time)
-        const uint64_t t1 = globaltimer_ns();
-        for (int i = 0; i < kStages; ++i)
-          if (issued_mask & (1u << i)) {
-            const uint32_t par = (issued_par >> i) & 1u;
-            const uint64_t t0 = globaltimer_ns();
-            while (rank == 0 && !mbar_try_wait(&full[i], par) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
-            }
+    }
+    if (*abort_flag) {
+      // every TMA issued here must land before the CTA exits (a pair's second CTA cannot see its own land: it gives
+      // them a time)
+      const uint64_t t1 = globaltimer_ns();
+      for (int i = 0; i < kStages; ++i)
+        if (issued_mask & (1u << i)) {
+          const uint32_t par = (issued_par >> i) & 1u;
+          while (rank == 0 && !mbar_try_wait(&full[i], par) && globaltimer_ns() - t1 < MOE_WAIT_NS) {
           }
-        while (CG == 2 && globaltimer_ns() - t1 < 1000000ull) {
         }
+      while (CG == 2 && globaltimer_ns() - t1 < 1000000ull) {
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ======================= MMA issuer
-    if (lane == 0 && rank == 0) {
+    // ======================= MMA issuer. Descriptors are those of the first stage plus the address / 16.
+    if (rank == 0) {
       constexpr uint32_t IDESC = idesc_bf16(CG * BM, BN, C::A_MN ? 1 : 0, C::B_MN ? 1 : 0);
+      constexpr int A_STEP = (C::A_MN ? 2048 : 32) >> 4, B_STEP = (C::B_MN ? 2048 : 32) >> 4;  // 16 of K
+      const uint32_t base = smem_u32(smem);
+      const uint64_t a0 = smem_desc_sw128(base, C::A_MN ? 64 * BK * 2 : 16, 1024);
+      const uint64_t b0 = smem_desc_sw128(base + A_BYTES, C::B_MN ? 64 * BK * 2 : 16, 1024);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       for (Seg s = walk.next(p); s.tile >= 0 && !aborted; s = walk.next(p)) {
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
+        if (!mbar_wait_warp(&tempty[acc], acc_phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
           aborted = true;
           break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         for (int kb = 0; kb < s.nkb; ++kb) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
+          if (!mbar_wait_warp(&full[stage], phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
             aborted = true;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + stage * C::STAGE_BYTES), b0 = a0 + A_BYTES;
+          if (elect_one()) {
+            const uint64_t ad = a0 + stage * (C::STAGE_BYTES >> 4), bd = b0 + stage * (C::STAGE_BYTES >> 4);
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = C::A_MN ? smem_desc_sw128(a0 + kk * 2048, 64 * BK * 2, 1024)
-                                        : smem_desc_sw128(a0 + kk * 32, 16, 1024);
-            const uint64_t bd = C::B_MN ? smem_desc_sw128(b0 + kk * 2048, 64 * BK * 2, 1024)
-                                        : smem_desc_sw128(b0 + kk * 32, 16, 1024);
-            mma<CG>(d_tmem, ad, bd, IDESC, (kb | kk) != 0 ? 1u : 0u);
+            for (int kk = 0; kk < BK / 16; ++kk)
+              mma<CG>(d_tmem, ad + kk * A_STEP, bd + kk * B_STEP, IDESC, (kb | kk) != 0 ? 1u : 0u);
+            commit<CG>(&empty[stage]);
           }
-          commit<CG>(&empty[stage]);
+          __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (aborted) break;
-        commit<CG>(&tfull[acc]);
+        if (elect_one()) commit<CG>(&tfull[acc]);
+        __syncwarp();
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1;
@@ -487,7 +490,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
       }
       if (*abort_flag) {
         // wait for every MMA already issued before TMEM is released
-        commit<CG>(drain);
+        if (elect_one()) commit<CG>(drain);
+        __syncwarp();
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
         }
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
         break;
       }
       tc_fence_after();
-      const Origin o = origin<OP, CG>(p, s.tile, rank);
+      const Origin o = origin<OP, CG, BN>(p, s.tile, rank);
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN;
       const int rows = o.rows - 32 * q;  // of this warp's 32 (may be <= 0)
       const long long row0 = (long long)o.m0 + 32 * q;
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
         }
       } else if constexpr (OP == OP_GATEUP) {
 #pragma unroll 1
-        for (int c = h * 64; c < (h + 1) * 64; c += 32) {
+        for (int c = h * (BN / 4); c < (h + 1) * (BN / 4); c += 32) {
           const int cols = o.cols - c;
           if (cols <= 0) break;  // warp-uniform
           float g[32], u[32];
@@ -604,7 +608,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
   if (CG == 2) pair_sync();  // everything the pair sends each other has arrived
   if (warp == 1) {
     tc_fence_after();
-    free_tmem<CG>(tmem_base);
+    free_tmem<CG>(tmem_base, 2 * BN);
   }
 }
 
@@ -613,7 +617,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
 // a fixed order (8 tiles in 18 pieces each: 17 us by one thread; 64 tiles in 2 or 3: 14 by four, 10.7 by one).
 constexpr int FIX_THREADS = 256;
 constexpr int MAX_PIECES = 16, MANY_PIECES = 6;
-template <int OP, int CG, int SPLIT>
+template <int OP, int CG, int BN, int SPLIT>
 __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constant__ Params p) {
   constexpr int NV = OP == OP_GATEUP ? 16 : 8, FIX_ITEMS = FIX_THREADS / SPLIT;
   __shared__ float sums[SPLIT > 1 ? SPLIT - 1 : 1][NV][FIX_ITEMS];
@@ -622,7 +626,7 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
   const int i = blockIdx.x / CG, rank = CG == 2 ? (int)blockIdx.x & 1 : 0;
   const int b0 = (int)((long long)i * p.KB / p.sk_per), b1 = (int)(((long long)(i + 1) * p.KB - 1) / p.sk_per);
   if (b0 == b1) return;  // one CTA (pair) held the whole tile and finished it
-  const Origin o = origin<OP, CG>(p, p.n_full + i, rank);
+  const Origin o = origin<OP, CG, BN>(p, p.n_full + i, rank);
   if (o.rows <= 0) return;
   const int part = threadIdx.x / FIX_ITEMS, item = threadIdx.x % FIX_ITEMS;
   const int total = (o.cols + 7) / 8 * o.rows;
@@ -745,7 +749,7 @@ int max_pairs() {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2 * (MAX_CTAS / 2));
     cfg.blockDim = dim3(NUM_THREADS);
-    cfg.dynamicSmemBytes = Cfg<OP, 2>::SMEM_BYTES;
+    cfg.dynamicSmemBytes = Cfg<OP, 2, 256>::SMEM_BYTES;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = 2;
@@ -753,7 +757,9 @@ int max_pairs() {
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, gemm_kernel<OP, 2>, &cfg) != cudaSuccess) {
+    if (cudaFuncSetAttribute(gemm_kernel<OP, 2, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<OP, 2, 256>::SMEM_BYTES) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, gemm_kernel<OP, 2, 256>, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();
       n = 0;
     }
@@ -762,49 +768,75 @@ int max_pairs() {
   return cached[dev] > 0 ? cached[dev] : 0;
 }
 
-template <int OP, int CG>
-int launch_cg(Params& p, int workers, cudaStream_t st, bool dep) {
-  using C = Cfg<OP, CG>;
-  const int per = (p.M + BM * CG - 1) / (BM * CG);
-  p.tiles_m = p.halves * per;
-  p.tm_split = per;
-  p.tiles_n = (p.N + C::N_STEP - 1) / C::N_STEP;
-  const long long total = (long long)p.tiles_m * p.tiles_n;
-  const int rest = (int)(total % workers);
-  // Cutting the rest along K saves (1 - rest / workers) of a tile's time, about 0.27 us per k-block (0.7 where rows
-  // do not start on 128 bytes: every row of a box is then on two lines), and costs about 6 us (partial sums out and
-  // in again, one more kernel).
-  const bool cut = rest && (long long)(workers - rest) * p.KB > (p.ragged ? 9ll : 22ll) * workers;
-  p.n_full = (int)(cut ? total - rest : total);
-  p.sk_tiles = cut ? rest : 0;
-  p.sk_per = cut ? std::max((rest * p.KB + workers - 1) / workers, (p.KB + MAX_PIECES - 1) / MAX_PIECES) : 0;
-  auto kern = gemm_kernel<OP, CG>;
-  int n = workers;
-  if (!cut && total < n) n = (int)total;
+// Form and work split of a product, chosen before its tensor maps are made (the form sets the boxes of B).
+struct Plan {
+  int cg, bn;
+  int workers;  // CTAs (pairs)
+  int b_box;    // rows of a K-major B box
+};
+
+// The form of least estimated time: rounds of tiles times k-blocks times a k-block's time, measured in us (down
+// projection, T = H = F = 4096, all in one launch: 97.9 us with one CTA and 256 columns, 109.0 with 128, pairs 82.1 and
+// 91.2; 24 k-blocks of T = 1001, H = 2048: 14.4, 11.6, 14.4 and 12.3). Cutting the tiles of the last round along K
+// saves the idle part of that round and costs partial sums out and in again and one more kernel, 6 to 10 us with 128
+// columns, 10 to 19 with 256 (T = 333, H = 2048, F = 5504 with 128: 24.6 us whole, 18.5 cut; T = 700: 25.0 and 26.7).
+template <int OP>
+Plan plan(Params& p) {
+  static constexpr float KB_US[2][2] = {{0.22f, 0.355f}, {0.185f, 0.29f}};  // [pairs][256 columns]
+  int sms = moe_host::num_sms();
+  if (sms > MAX_CTAS) sms = MAX_CTAS;
+  const int pairs = std::min(max_pairs<OP>(), sms / 2);
+  Plan c{};
+  float best = 1e30f;
+  for (int cg = 1; cg <= 2; ++cg) {
+    const int workers = cg == 2 ? pairs : sms;
+    if (workers == 0) continue;
+    const int per = (p.M + BM * cg - 1) / (BM * cg), tiles_m = p.halves * per;
+    for (int bn = 128; bn <= 256; bn *= 2) {
+      const int step = OP == OP_GATEUP ? bn / 2 : bn;
+      const int tiles_n = (p.N + step - 1) / step;
+      const long long total = (long long)tiles_m * tiles_n, rounds = total / workers;
+      const int rest = (int)(total % workers);
+      const float tile = p.KB * KB_US[cg - 1][bn / 256], cost = bn == 256 ? 12.f : 9.f;
+      const float whole = (rounds + (rest ? 1 : 0)) * tile, split = (rounds + (float)rest / workers) * tile + cost;
+      const bool cut = rest && split < whole;
+      if (std::min(whole, split) >= best) continue;
+      best = std::min(whole, split);
+      c = {cg, bn, workers, OP == OP_GATEUP ? bn / 2 : std::min(128, bn / cg)};
+      p.tiles_m = tiles_m;
+      p.tm_split = per;
+      p.tiles_n = tiles_n;
+      p.n_full = (int)(cut ? total - rest : total);
+      p.sk_tiles = cut ? rest : 0;
+      p.sk_per = cut ? std::max((rest * p.KB + workers - 1) / workers, (p.KB + MAX_PIECES - 1) / MAX_PIECES) : 0;
+    }
+  }
+  return c;
+}
+
+template <int OP, int CG, int BN>
+int launch_form(const Params& p, int workers, cudaStream_t st, bool dep) {
+  using C = Cfg<OP, CG, BN>;
+  auto kern = gemm_kernel<OP, CG, BN>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  const int n = p.sk_tiles || p.n_full > workers ? workers : p.n_full;
   int rc = launch_dep(kern, dim3(n * CG), NUM_THREADS, C::SMEM_BYTES, CG, st, p, dep);
-  if (rc || !cut) return rc;
-  const int per_tile = OP == OP_GATEUP ? 8 : 16;  // CTAs, one item per thread
+  if (rc || !p.sk_tiles) return rc;
+  const int per_tile = BM * C::N_STEP / 8 / FIX_THREADS;  // CTAs, one item per thread
   if (p.KB > MANY_PIECES * p.sk_per)
-    return launch_dep(fixup_kernel<OP, CG, 4>, dim3(rest * CG, 4 * per_tile), FIX_THREADS, 0, 1, st, p, true);
-  return launch_dep(fixup_kernel<OP, CG, 1>, dim3(rest * CG, per_tile), FIX_THREADS, 0, 1, st, p, true);
+    return launch_dep(fixup_kernel<OP, CG, BN, 4>, dim3(p.sk_tiles * CG, 4 * per_tile), FIX_THREADS, 0, 1, st, p, true);
+  return launch_dep(fixup_kernel<OP, CG, BN, 1>, dim3(p.sk_tiles * CG, per_tile), FIX_THREADS, 0, 1, st, p, true);
 }
 
 // dep: the kernel before it in the stream is one of the same call's.
 template <int OP>
-int launch(Params& p, cudaStream_t st, bool dep) {
-  if (cudaFuncSetAttribute(gemm_kernel<OP, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Cfg<OP, 1>::SMEM_BYTES) != cudaSuccess ||
-      cudaFuncSetAttribute(gemm_kernel<OP, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Cfg<OP, 2>::SMEM_BYTES) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return MOE_ERR_CUDA;
-  }
-  int sms = moe_host::num_sms();
-  if (sms > MAX_CTAS) sms = MAX_CTAS;
-  const int m1 = (p.M + BM - 1) / BM, m2 = (p.M + 2 * BM - 1) / (2 * BM) * 2;
-  const int pairs = max_pairs<OP>();
-  if (m2 * 16 <= m1 * 17 && 2 * pairs >= sms - 2) return launch_cg<OP, 2>(p, pairs < sms / 2 ? pairs : sms / 2, st, dep);
-  return launch_cg<OP, 1>(p, sms, st, dep);
+int launch(const Params& p, const Plan& c, cudaStream_t st, bool dep) {
+  if (c.cg == 2)
+    return c.bn == 256 ? launch_form<OP, 2, 256>(p, c.workers, st, dep) : launch_form<OP, 2, 128>(p, c.workers, st, dep);
+  return c.bn == 256 ? launch_form<OP, 1, 256>(p, c.workers, st, dep) : launch_form<OP, 1, 128>(p, c.workers, st, dep);
 }
 
 }  // namespace dense

@@ -191,9 +191,8 @@ static bool tmap(CUtensorMap* m, Mat a, long long inner, long long outer, int bo
                                   box_outer);
 }
 
-static Params base_params(int M, int N, int KB, Mat A, Mat B, float* part, void* C, long long ldc) {
+static Params base_params(int M, int N, int KB, float* part, void* C, long long ldc) {
   Params p{};
-  p.ragged = A.ld % 64 != 0 || B.ld % 64 != 0;
   p.M = M;
   p.N = N;
   p.KB = KB;
@@ -207,57 +206,62 @@ static Params base_params(int M, int N, int KB, Mat A, Mat B, float* part, void*
 
 static int gateup(int T, int H, int F, Mat x, Mat Wg, Mat Wu, __nv_bfloat16* a, const Saved& s, float* part,
                   cudaStream_t st, bool dep) {
-  Params p = base_params(T, F, cdiv(H, dense::BK), x, Wg, part, a, pad64(F));
-  if (!tmap(&p.tmA, x, H, T, 128) || !tmap(&p.tmB0, Wg, H, F, 128) || !tmap(&p.tmB1, Wu, H, F, 128))
+  Params p = base_params(T, F, cdiv(H, dense::BK), part, a, pad64(F));
+  const dense::Plan c = dense::plan<dense::OP_GATEUP>(p);
+  if (!tmap(&p.tmA, x, H, T, 128) || !tmap(&p.tmB0, Wg, H, F, c.b_box) || !tmap(&p.tmB1, Wu, H, F, c.b_box))
     return MOE_ERR_CUDA;
   p.save_hi = s.hi;
   p.save_lo = s.lo;
   p.ld2 = 2LL * pad64(F);
   p.up = pad64(F);
-  return dense::launch<dense::OP_GATEUP>(p, st, dep);
+  return dense::launch<dense::OP_GATEUP>(p, c, st, dep);
 }
 
 static int down(int T, int H, int F, const __nv_bfloat16* a, Mat Wd, void* y, float* part, cudaStream_t st, bool dep) {
   const Mat am{a, pad64(F)};
-  Params p = base_params(T, H, cdiv(F, dense::BK), am, Wd, part, y, H);
-  if (!tmap(&p.tmA, am, F, T, 128) || !tmap(&p.tmB0, Wd, F, H, 128)) return MOE_ERR_CUDA;
-  return dense::launch<dense::OP_DOWN>(p, st, dep);
+  Params p = base_params(T, H, cdiv(F, dense::BK), part, y, H);
+  const dense::Plan c = dense::plan<dense::OP_DOWN>(p);
+  if (!tmap(&p.tmA, am, F, T, 128) || !tmap(&p.tmB0, Wd, F, H, c.b_box)) return MOE_ERR_CUDA;
+  return dense::launch<dense::OP_DOWN>(p, c, st, dep);
 }
 
 static int dgrad_act(int T, int H, int F, Mat dY, Mat Wd, const Saved& s, __nv_bfloat16* dgu, float* part,
                      cudaStream_t st, bool dep) {
-  Params p = base_params(T, F, cdiv(H, dense::BK), dY, Wd, part, dgu, 0);
+  Params p = base_params(T, F, cdiv(H, dense::BK), part, dgu, 0);
+  const dense::Plan c = dense::plan<dense::OP_DGRAD_ACT>(p);
   if (!tmap(&p.tmA, dY, H, T, 128) || !tmap(&p.tmB0, Wd, F, H, 64)) return MOE_ERR_CUDA;
   p.save_hi = s.hi;
   p.save_lo = s.lo;
   p.ld2 = 2LL * pad64(F);
   p.up = pad64(F);
-  return dense::launch<dense::OP_DGRAD_ACT>(p, st, dep);
+  return dense::launch<dense::OP_DGRAD_ACT>(p, c, st, dep);
 }
 
 static int dgrad_x(int T, int H, int F, const __nv_bfloat16* dgu, Mat Wg, Mat Wu, void* dX, float* part,
                    cudaStream_t st, bool dep) {
   const int kb = cdiv(F, dense::BK);
   const Mat dg{dgu, 2LL * pad64(F)}, du{dgu + pad64(F), 2LL * pad64(F)};
-  Params p = base_params(T, H, 2 * kb, dg, Wg, part, dX, H);
+  Params p = base_params(T, H, 2 * kb, part, dX, H);
+  const dense::Plan c = dense::plan<dense::OP_DGRAD_X>(p);
   p.kb_split = kb;
   if (!tmap(&p.tmA, dg, F, T, 128) || !tmap(&p.tmA2, du, F, T, 128) || !tmap(&p.tmB0, Wg, H, F, 64) ||
       !tmap(&p.tmB1, Wu, H, F, 64))
     return MOE_ERR_CUDA;
-  return dense::launch<dense::OP_DGRAD_X>(p, st, dep);
+  return dense::launch<dense::OP_DGRAD_X>(p, c, st, dep);
 }
 
 // dW [M, N] = sum_t dO[t, :M]^T act[t, :N]; with dO2, a second [M, N] from it into dW2 in the same launch.
 static int wgrad(int T, int M, int N, Mat dO, Mat dO2, Mat act, void* dW, void* dW2, float* part, cudaStream_t st,
                  bool dep) {
-  Params p = base_params(M, N, cdiv(T, dense::BK), dO, act, part, dW, N);
+  Params p = base_params(M, N, cdiv(T, dense::BK), part, dW, N);
+  p.halves = dO2.p ? 2 : 1;
+  const dense::Plan c = dense::plan<dense::OP_WGRAD>(p);
   if (!tmap(&p.tmA, dO, M, T, 64) || !tmap(&p.tmB0, act, N, T, 64)) return MOE_ERR_CUDA;
   if (dO2.p) {
     if (!tmap(&p.tmA2, dO2, M, T, 64)) return MOE_ERR_CUDA;
-    p.halves = 2;
     p.C2 = static_cast<__nv_bfloat16*>(dW2);
   }
-  return dense::launch<dense::OP_WGRAD>(p, st, dep);
+  return dense::launch<dense::OP_WGRAD>(p, c, st, dep);
 }
 
 // One product of the streaming path: W1 for gate/up, scales for MXFP8; x has rows of ldx elements, out of ldo.

@@ -42,6 +42,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "elect.cuh"
 #include "gemm_mx.cuh"
 #include "swiglu.cuh"
 
@@ -259,126 +260,126 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
   bool aborted = false;
   if (warp == 0) {
     // ======================= TMA producer
-    if (lane == 0) {
-      const uint32_t tx = (uint32_t)(((GATEUP ? 2 : 1) * p.r + p.T) * p.s * ROW_BYTES);
-      const int kstep = MX ? 128 : 64;
-      int stage = 0;
-      uint32_t phase = 0, issued_mask = 0, issued_par = 0;
-      // the ks-th stage of K: coordinate along K, or the block's number where the maps are cut along it
-      const auto load = [&](const CUtensorMap* m, int row, int ks, uint8_t* dst, uint64_t* bar) {
-        const int kb = ks * p.s;
-        tma_load_3d(dst, m, p.z ? 0 : kb * kstep, row, p.z ? kb : 0, bar);
-      };
-      const auto load_w = [&](int t, int ks, int st) {
-        uint8_t* b = ring + st * p.stage_bytes;
-        load(&p.tmW0, t * p.r, ks, b, &full[st]);
-        if (GATEUP) load(&p.tmW1, t * p.r, ks, b + w_bytes, &full[st]);
-      };
-      // the first weights, before the wait for the kernel that makes x
-      // (where there is none, a stage's tokens go out with its weights: behind the whole ring's they would be late)
-      const int ahead = p.early ? min(p.stages, ks1 - ks0) : 0;
-      for (int st = 0; st < ahead; ++st) {
-        mbar_arrive_expect_tx(&full[st], tx);
-        issued_mask |= 1u << st;
-        load_w(tile0, ks0 + st, st);
-      }
-      if (with_tail) {
-        mbar_arrive_expect_tx(tail_full, (uint32_t)(((GATEUP ? 2 : 1) * p.r + p.T) * ROW_BYTES));
-        tma_load_2d(tail, &p.tmW0t, p.KB * kstep, tile0 * p.r, tail_full);
-        if (GATEUP) tma_load_2d(tail + p.r8 * ROW_BYTES, &p.tmW1t, p.KB * kstep, tile0 * p.r, tail_full);
-      }
-      griddep_wait();
-      if (with_tail) tma_load_2d(tail + (GATEUP ? 2 : 1) * p.r8 * ROW_BYTES, &p.tmXt, p.KB * kstep, 0, tail_full);
-      for (int t = tile0; t < p.tiles && !aborted; t += tile_step) {
-        for (int ks = ks0; ks < ks1; ++ks) {
-          const bool early = t == tile0 && ks < ks0 + ahead;
-          if (!early) {
-            if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) {
-              aborted = true;
-              break;
-            }
-            mbar_arrive_expect_tx(&full[stage], tx);
-            issued_mask |= 1u << stage;
-            issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-            load_w(t, ks, stage);
+    const uint32_t tx = (uint32_t)(((GATEUP ? 2 : 1) * p.r + p.T) * p.s * ROW_BYTES);
+    const int kstep = MX ? 128 : 64;
+    int stage = 0;
+    uint32_t phase = 0, issued_mask = 0, issued_par = 0;
+    // the ks-th stage of K: coordinate along K, or the block's number where the maps are cut along it
+    const auto load = [&](const CUtensorMap* m, int row, int ks, uint8_t* dst, uint64_t* bar) {
+      const int kb = ks * p.s;
+      tma_load_3d(dst, m, p.z ? 0 : kb * kstep, row, p.z ? kb : 0, bar);
+    };
+    const auto load_w = [&](int t, int ks, int st) {
+      uint8_t* b = ring + st * p.stage_bytes;
+      mbar_arrive_expect_tx(&full[st], tx);
+      load(&p.tmW0, t * p.r, ks, b, &full[st]);
+      if (GATEUP) load(&p.tmW1, t * p.r, ks, b + w_bytes, &full[st]);
+    };
+    // the first weights, before the wait for the kernel that makes x (where there is none, a stage's tokens go out
+    // with its weights: behind the whole ring's they would be late)
+    const int ahead = p.early ? min(p.stages, ks1 - ks0) : 0;
+    for (int st = 0; st < ahead; ++st) {
+      issued_mask |= 1u << st;
+      if (elect_one()) load_w(tile0, ks0 + st, st);
+    }
+    if (with_tail && elect_one()) {
+      mbar_arrive_expect_tx(tail_full, (uint32_t)(((GATEUP ? 2 : 1) * p.r + p.T) * ROW_BYTES));
+      tma_load_2d(tail, &p.tmW0t, p.KB * kstep, tile0 * p.r, tail_full);
+      if (GATEUP) tma_load_2d(tail + p.r8 * ROW_BYTES, &p.tmW1t, p.KB * kstep, tile0 * p.r, tail_full);
+    }
+    __syncwarp();
+    griddep_wait();
+    if (with_tail && elect_one())
+      tma_load_2d(tail + (GATEUP ? 2 : 1) * p.r8 * ROW_BYTES, &p.tmXt, p.KB * kstep, 0, tail_full);
+    __syncwarp();
+    for (int t = tile0; t < p.tiles && !aborted; t += tile_step) {
+      for (int ks = ks0; ks < ks1; ++ks) {
+        const bool early = t == tile0 && ks < ks0 + ahead;
+        if (!early) {
+          if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) {
+            aborted = true;
+            break;
           }
+          issued_mask |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        }
+        if (elect_one()) {
+          if (!early) load_w(t, ks, stage);
           load(&p.tmX, 0, ks, ring + stage * p.stage_bytes + x_off, &full[stage]);
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1;
-          }
+        }
+        __syncwarp();
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      if (GATEUP)
-        for (int ks = p.next_from; ks < p.next_to && !aborted; ++ks)
-          for (int t = blockIdx.x; t < p.next_tiles; t += gridDim.x)
-            tma_prefetch_3d(&p.tmNext, 0, t * p.next_r, ks * p.next_s);
-      if (*abort_flag) {
-        // every TMA this thread issued must land before the CTA exits (a stage whose tokens were not asked for any
-        // more never completes: the wait is bounded)
-        const uint64_t t0 = globaltimer_ns();
-        for (int i = 0; i < p.stages; ++i)
-          if (issued_mask & (1u << i)) {
-            const uint32_t par = (issued_par >> i) & 1u;
-            while (!mbar_try_wait(&full[i], par) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
-            }
+    }
+    if (GATEUP && elect_one())
+      for (int ks = p.next_from; ks < p.next_to && !aborted; ++ks)
+        for (int t = blockIdx.x; t < p.next_tiles; t += gridDim.x)
+          tma_prefetch_3d(&p.tmNext, 0, t * p.next_r, ks * p.next_s);
+    __syncwarp();
+    if (*abort_flag) {
+      // every TMA issued here must land before the CTA exits (a stage whose tokens were not asked for any more never
+      // completes: the wait is bounded)
+      const uint64_t t0 = globaltimer_ns();
+      for (int i = 0; i < p.stages; ++i)
+        if (issued_mask & (1u << i)) {
+          const uint32_t par = (issued_par >> i) & 1u;
+          while (!mbar_try_wait(&full[i], par) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
           }
-      }
+        }
     }
     __syncwarp();
   } else if (warp == 1 || (ISSUERS == 2 && warp == 3)) {
-    // ======================= MMA issuers: single threads, whose instructions set the pace, so everything that does
-    // not change from stage to stage is kept: descriptors are a constant plus the address / 16
-    if (lane == 0) {
-      const int me = warp >> 1;
-      const bool two = GATEUP && !p.merged;
-      const uint64_t desc0 = smem_desc_sw128(0, 16, 1024) + (smem_u32(ring) >> 4);
-      const uint64_t sdesc0 = ggmx::sf_desc(0) + (smem_u32(sf_ring) >> 4);
-      const uint32_t stage16 = p.stage_bytes >> 4, w16 = w_bytes >> 4, x16 = x_off >> 4;
-      int slot = 0;
-      uint32_t sphase = 0;
-      const uint32_t sf_tmem = tmem_base + p.acc_bufs * ISSUERS * p.acc_cols + me * 2 * SF_SLOT_COLS;
-      uint32_t id[4];
+    // ======================= MMA issuers. Descriptors are those of the first stage plus the address / 16.
+    const int me = warp >> 1;
+    const bool two = GATEUP && !p.merged;
+    const uint64_t desc0 = smem_desc_sw128(smem_u32(ring), 16, 1024);
+    const uint64_t sdesc0 = ggmx::sf_desc(smem_u32(sf_ring));
+    const uint32_t stage16 = p.stage_bytes >> 4, w16 = w_bytes >> 4, x16 = x_off >> 4;
+    const uint32_t sf_tmem = tmem_base + p.acc_bufs * ISSUERS * p.acc_cols + me * 2 * SF_SLOT_COLS;
+    uint32_t id[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) id[q] = idesc<MX>(p.mma_n, q);
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      for (int t = tile0; t < p.tiles && !aborted; t += tile_step) {
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
+    for (int q = 0; q < 4; ++q) id[q] = idesc<MX>(p.mma_n, q);
+    int stage = 0, slot = 0, acc = 0;
+    uint32_t phase = 0, sphase = 0, acc_phase = 0;
+    const auto step = [&] {
+      if (MX && ++slot == SF_SLOTS) {
+        slot = 0;
+        sphase ^= 1;
+      }
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    };
+    for (int t = tile0; t < p.tiles && !aborted; t += tile_step) {
+      if (!mbar_wait_warp(&tempty[acc], acc_phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d0 = tmem_base + (acc * ISSUERS + me) * p.acc_cols, d1 = d0 + p.mma_n;
+      bool first = true, slot2 = false;
+      for (int ks = ks0; ks < ks1; ++ks) {
+        if (ISSUERS == 2 && (stage & 1) != me) {  // the other issuer's
+          step();
+          continue;
+        }
+        if ((MX && !mbar_wait_warp(&sfull[slot], sphase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) ||
+            !mbar_wait_warp(&full[stage], phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
           aborted = true;
           break;
         }
         tc_fence_after();
-        const uint32_t d0 = tmem_base + (acc * ISSUERS + me) * p.acc_cols, d1 = d0 + p.mma_n;
-        bool first = true, slot2 = false;
-        uint64_t ad = desc0 + stage * stage16;
-        for (int ks = ks0; ks < ks1; ++ks) {
-          if (ISSUERS == 2 && (stage & 1) != me) {  // the other issuer's
-            if (MX && ++slot == SF_SLOTS) {
-              slot = 0;
-              sphase ^= 1;
-            }
-            ad += stage16;
-            if (++stage == p.stages) {
-              stage = 0;
-              phase ^= 1;
-              ad = desc0;
-            }
-            continue;
-          }
-          if ((MX && !mbar_wait(&sfull[slot], sphase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) ||
-              !mbar_wait(&full[stage], phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
-            aborted = true;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t bd = ad + x16;
-          // scale slots of TMEM alternate: the copies of a stage follow, in issue order, the MMAs that read
-          // the slot two stages ago
+        if (MX) fence_proxy_async_smem();  // the scales were written by ordinary copies, and are read by tcgen05.cp
+        if (elect_one()) {
+          const uint64_t ad = desc0 + stage * stage16, bd = ad + x16;
+          // scale slots of TMEM alternate: the copies of a stage follow, in issue order, the MMAs that read the slot
+          // two stages ago
           const uint32_t sc = sf_tmem + (slot2 ? SF_SLOT_COLS : 0);
-          slot2 = !slot2;
           if (MX) {
-            fence_proxy_async_smem();  // the scales were written by ordinary copies, and are read by tcgen05.cp
             const uint64_t sd = sdesc0 + slot * (p.sf_bytes >> 4), sx = sd + (p.sf_x >> 4);
             ggmx::tmem_cp_32x128b_x4(sc, sd);
             if (two) ggmx::tmem_cp_32x128b_x4(sc + 4, sd + (512 >> 4));
@@ -403,30 +404,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
 #pragma unroll
             for (int q = 0; q < 4; ++q) mma(d0, ad, sc, q);
           }
-          first = false;
           mma_commit(&empty[stage]);
-          if (MX) {
-            mma_commit(&sempty[slot]);
-            if (++slot == SF_SLOTS) {
-              slot = 0;
-              sphase ^= 1;
-            }
-          }
-          ad += stage16;
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1;
-            ad = desc0;
-          }
+          if (MX) mma_commit(&sempty[slot]);
         }
-        if (aborted) break;
-        if (with_tail && me == 0) {
-          // into accumulators of its own: its operands' rows are not stacked
-          if (!mbar_wait(tail_full, 0, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
-            aborted = true;
-            break;
-          }
-          tc_fence_after();
+        __syncwarp();
+        slot2 = !slot2;
+        first = false;
+        step();
+      }
+      if (aborted) break;
+      if (with_tail && me == 0) {
+        // into accumulators of its own: its operands' rows are not stacked
+        if (!mbar_wait_warp(tail_full, 0, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
+          aborted = true;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
           const uint64_t at = smem_desc_sw128(smem_u32(tail), 16, 1024), wt = p.r8 * ROW_BYTES >> 4;
           const uint64_t bt = at + (GATEUP ? 2 : 1) * wt;
           const uint32_t dt = tmem_base + p.acc_bufs * ISSUERS * p.acc_cols, idt = idesc<MX>(p.tail_n, 0);
@@ -436,18 +430,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
             if (two) mma_bf16(dt + p.tail_n, at + wt + 2 * q, bt + 2 * q, idt, q != 0 ? 1u : 0u);
           }
         }
-        mma_commit(&tfull[acc]);
-        if (++acc == p.acc_bufs) {
-          acc = 0;
-          acc_phase ^= 1;
-        }
+        __syncwarp();
       }
-      if (*abort_flag) {
-        // wait for every MMA already issued before TMEM is released
-        mma_commit(&drain[me]);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(&drain[me], 0) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
-        }
+      if (elect_one()) mma_commit(&tfull[acc]);
+      __syncwarp();
+      if (++acc == p.acc_bufs) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+    if (*abort_flag) {
+      // wait for every MMA already issued before TMEM is released
+      if (elect_one()) mma_commit(&drain[me]);
+      __syncwarp();
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&drain[me], 0) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
       }
     }
     __syncwarp();
