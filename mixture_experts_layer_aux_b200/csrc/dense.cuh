@@ -30,6 +30,7 @@
 
 #include "common.cuh"
 #include "elect.cuh"
+#include "gemm_mx.cuh"
 #include "swiglu.cuh"
 
 namespace dense {
@@ -41,6 +42,7 @@ constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int STG_ROW = 80;  // staging: 32 rows x (64 + 16) bytes per epilogue warp
 constexpr int STG_BYTES = EPI_WARPS * 32 * STG_ROW;
 constexpr int BAR_BYTES = 256;
+constexpr int SF_KB = 4, SF_BUFS = 3;  // MXFP8: k-blocks in a batch of scales, batches in shared memory
 constexpr int MAX_CTAS = 160;                            // CTAs of one launch (one per SM)
 constexpr size_t SLOT_FLOATS = (size_t)BM * MAX_BN;          // one CTA's partial accumulator
 constexpr size_t PART_BYTES = 2ull * MAX_CTAS * SLOT_FLOATS * sizeof(float);
@@ -51,12 +53,16 @@ enum Op : int {
   OP_DGRAD_ACT = 2,  // A = dY K-major, B = W_d MN-major: dgate | dup from the saved gate/up
   OP_DGRAD_X = 3,    // A = dgate then dup (K-major), B = W_g then W_u (MN-major): bf16
   OP_WGRAD = 4,      // A = dO^T, B = act^T (both MN-major): bf16; rows past m_split from A2 into C2
+  OP_GATEUP_MX = 5,  // the first two in MXFP8: e4m3 operands with a scale per 1x32 block, the activation as such
+  OP_DOWN_MX = 6,
 };
+constexpr bool is_mx(int op) { return op >= OP_GATEUP_MX; }
+constexpr bool is_gateup(int op) { return op == OP_GATEUP || op == OP_GATEUP_MX; }
 
 struct __align__(64) Params {
   CUtensorMap tmA, tmA2, tmB0, tmB1;
   int M, N;            // output rows and columns (per half when m_split)
-  int KB;              // k-blocks of 64
+  int KB;              // k-blocks of 128 bytes
   int kb_split;        // OP_DGRAD_X: k-blocks of the first half
   int halves;          // OP_WGRAD: 2 for two stacked outputs of M rows each (A2, C2 the second), else 1
   int tiles_m, tiles_n;
@@ -74,6 +80,12 @@ struct __align__(64) Params {
   uint8_t* save_lo;
   long long ld2;
   int up;
+  // MXFP8: scales [rows, ld_sf] of A and B, read 16 bytes at a time when sf16; OP_GATEUP_MX writes e4m3 to C and scales
+  // [M, N / 32] to C_sf
+  const uint8_t *sfa, *sfb0, *sfb1;
+  long long ld_sf;
+  int sf16;
+  uint8_t* C_sf;
   int* status;
 };
 
@@ -118,13 +130,21 @@ template <int OP, int CG, int BN_>
 struct Cfg {
   static constexpr int BN = BN_;
   static constexpr bool A_MN = OP == OP_WGRAD;
-  static constexpr bool B_MN = OP >= OP_DGRAD_ACT;
-  static constexpr int N_STEP = OP == OP_GATEUP ? BN / 2 : BN;  // output columns per tile
+  static constexpr bool B_MN = OP >= OP_DGRAD_ACT && OP <= OP_WGRAD;
+  static constexpr bool MX = is_mx(OP), GATEUP = is_gateup(OP);
+  static constexpr int N_STEP = GATEUP ? BN / 2 : BN;           // output columns per tile
   static constexpr int B_ROWS = BN / CG;                        // of B, per CTA
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK * 2;
-  static constexpr int kStages = BN == 128 ? (CG == 2 ? 8 : 6) : CG == 2 ? 6 : 4;
-  static constexpr int SMEM_BYTES = 1024 + kStages * STAGE_BYTES + BAR_BYTES + STG_BYTES;
-  static constexpr int B_BOX = OP == OP_GATEUP ? BN / 2 : B_ROWS < 128 ? B_ROWS : 128;  // rows of a K-major B box
+  static constexpr int kStages = (BN == 128 ? (CG == 2 ? 8 : 6) : CG == 2 ? 6 : 4) - (MX ? 1 : 0);
+  static constexpr int THREADS = NUM_THREADS + (MX ? 32 : 0);   // MXFP8: one warp for the scales
+  static constexpr int SF_BLOCKS = (BM + BN) / 128;             // MXFP8: 512-byte scale chunks of a k-block
+  static constexpr int SF_BATCH_BYTES = MX ? SF_KB * SF_BLOCKS * 512 : 0;
+  static constexpr int SMEM_BYTES = 1024 + kStages * STAGE_BYTES + SF_BUFS * SF_BATCH_BYTES + STG_BYTES + BAR_BYTES;
+  static constexpr int B_BOX = GATEUP ? BN / 2 : B_ROWS < 128 ? B_ROWS : 128;  // rows of a K-major B box
+  // TMEM: accumulators, then two slots of scales (4 columns per chunk)
+  static constexpr int ACCS = MX && BN == 256 ? 1 : 2;
+  static constexpr int TMEM_COLS = MX ? 512 : 2 * BN;
+  static_assert(!MX || ACCS * BN + 8 * SF_BLOCKS <= 512, "TMEM");
   static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
@@ -181,6 +201,26 @@ MOE_DEV void mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+template <int CG>
+MOE_DEV void mma_mx(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                    uint32_t accumulate) {
+  if constexpr (CG == 1)
+    ggmx::mma_mxf8(d_tmem, adesc, bdesc, idesc, sfa, sfb, accumulate);
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], p; }" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+// One chunk of scales (128 rows x 4 bytes) to 4 columns of TMEM; a pair: of both CTAs, each from its own.
+template <int CG>
+MOE_DEV void copy_sf(uint32_t taddr, uint64_t sdesc) {
+  if constexpr (CG == 1)
+    ggmx::tmem_cp_32x128b_x4(taddr, sdesc);
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
 // Arrives on the barrier (of both CTAs of a pair) once every MMA issued so far is done.
 template <int CG>
 MOE_DEV void commit(uint64_t* bar) {
@@ -193,6 +233,12 @@ MOE_DEV void commit(uint64_t* bar) {
                        pair_addr(smem_u32(bar), r))
                    : "memory");
   }
+}
+// mbar_wait_warp on a barrier that ordinary writes of the pair's other CTA are behind.
+MOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int code) {
+  if (!mbar_wait_warp(bar, parity, abort, status, code)) return false;
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return true;
 }
 // Arrives on the first CTA's barrier.
 template <int CG>
@@ -323,18 +369,21 @@ MOE_DEV void pack32(const float (&v)[32], uint32_t (&w)[16]) {
 }
 
 template <int OP, int CG, int BN>
-__global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const __grid_constant__ Params p) {
   using C = Cfg<OP, CG, BN>;
   constexpr int kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* stg_area = smem + kStages * C::STAGE_BYTES;
+  uint8_t* sf_ring = smem + kStages * C::STAGE_BYTES;
+  uint8_t* stg_area = sf_ring + SF_BUFS * C::SF_BATCH_BYTES;
   uint64_t* full = reinterpret_cast<uint64_t*>(stg_area + STG_BYTES);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* sfull = drain + 1;
+  uint64_t* sempty = sfull + SF_BUFS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + SF_BUFS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -348,6 +397,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], CG * EPI_WARPS);
     }
+    for (int i = 0; C::MX && i < SF_BUFS; ++i) {
+      mbar_init(&sfull[i], CG);
+      mbar_init(&sempty[i], 1);
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -356,7 +409,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
     tma_prefetch_desc(&p.tmA);
     tma_prefetch_desc(&p.tmB0);
   }
-  if (warp == 1) alloc_tmem<CG>(tmem_slot, 2 * BN);
+  if (warp == 1) alloc_tmem<CG>(tmem_slot, C::TMEM_COLS);
   __syncthreads();
   if (CG == 2) pair_sync();  // both CTAs' barriers exist before either signals the other
   tc_fence_after();
@@ -373,7 +426,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
     uint32_t phase = 0, issued_mask = 0, issued_par = 0;
     for (Seg s = walk.next(p); s.tile >= 0 && !aborted; s = walk.next(p)) {
       const Origin o = origin<OP, CG, BN>(p, s.tile, rank);
-      const int b0 = o.n0 + (OP == OP_GATEUP ? 0 : rank * C::B_ROWS);
+      const int b0 = o.n0 + (C::GATEUP ? 0 : rank * C::B_ROWS);
       for (int kb = s.kb0; kb < s.kb0 + s.nkb; ++kb) {
         if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) {
           aborted = true;
@@ -387,7 +440,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
           uint8_t* sB = sA + A_BYTES;
           uint64_t* bar = &full[stage];
           const bool hi = OP == OP_DGRAD_X && kb >= p.kb_split;  // the up half of K
-          const int kc = (kb - (hi ? p.kb_split : 0)) * BK;
+          const int kc = (kb - (hi ? p.kb_split : 0)) * (C::MX ? 128 : BK);
           const CUtensorMap* mA = (hi || o.second) ? &p.tmA2 : &p.tmA;
           if constexpr (!C::A_MN) {
             load_tile<CG>(sA, mA, kc, o.m0, bar);
@@ -395,7 +448,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
             load_tile<CG>(sA, mA, o.m0, kc, bar);
             load_tile<CG>(sA + 64 * BK * 2, mA, o.m0 + 64, kc, bar);
           }
-          if constexpr (OP == OP_GATEUP) {
+          if constexpr (C::GATEUP) {
             // the first half of the accumulator's columns is gate, the second up
             if constexpr (CG == 2) {
               load_tile<CG>(sB, rank ? &p.tmB1 : &p.tmB0, kc, b0, bar);
@@ -448,6 +501,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
     // ======================= MMA issuer. Descriptors are those of the first stage plus the address / 16.
     if (rank == 0) {
       constexpr uint32_t IDESC = idesc_bf16(CG * BM, BN, C::A_MN ? 1 : 0, C::B_MN ? 1 : 0);
+      const uint64_t sd0 = C::MX ? ggmx::sf_desc(smem_u32(sf_ring)) : 0;
+      const uint32_t sf_tmem = tmem_base + C::ACCS * BN;
+      int buf = 0, slot = 0;
+      uint32_t buf_phase = 0;
       constexpr int A_STEP = (C::A_MN ? 2048 : 32) >> 4, B_STEP = (C::B_MN ? 2048 : 32) >> 4;  // 16 of K
       const uint32_t base = smem_u32(smem);
       const uint64_t a0 = smem_desc_sw128(base, C::A_MN ? 64 * BK * 2 : 16, 1024);
@@ -466,15 +523,41 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
             aborted = true;
             break;
           }
+          const int in_batch = (s.kb0 + kb) % SF_KB;
+          if (C::MX && (kb == 0 || in_batch == 0)) {
+            if (!mbar_wait_cluster(&sfull[buf], buf_phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
+              aborted = true;
+              break;
+            }
+          }
           tc_fence_after();
+          const bool sf_done = C::MX && (in_batch == SF_KB - 1 || kb == s.nkb - 1);
           if (elect_one()) {
             const uint64_t ad = a0 + stage * (C::STAGE_BYTES >> 4), bd = b0 + stage * (C::STAGE_BYTES >> 4);
+            if constexpr (C::MX) {
+              // slots alternate: the copies into one follow, in issue order, the MMAs that read it two k-blocks ago
+              const uint32_t sc = sf_tmem + slot * 4 * C::SF_BLOCKS;
+              const uint64_t sd = sd0 + ((buf * C::SF_BATCH_BYTES + in_batch * C::SF_BLOCKS * 512) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)
-              mma<CG>(d_tmem, ad + kk * A_STEP, bd + kk * B_STEP, IDESC, (kb | kk) != 0 ? 1u : 0u);
+              for (int i = 0; i < C::SF_BLOCKS; ++i) copy_sf<CG>(sc + 4 * i, sd + i * (512 >> 4));
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mma_mx<CG>(d_tmem, ad + 2 * q, bd + 2 * q, ggmx::idesc_mx(CG * BM, BN, q), sc | ((uint32_t)q << 30),
+                           (sc + 4) | ((uint32_t)q << 30), (kb | q) != 0 ? 1u : 0u);
+              if (sf_done) commit<CG>(&sempty[buf]);
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk)
+                mma<CG>(d_tmem, ad + kk * A_STEP, bd + kk * B_STEP, IDESC, (kb | kk) != 0 ? 1u : 0u);
+            }
             commit<CG>(&empty[stage]);
           }
           __syncwarp();
+          slot ^= 1;
+          if (sf_done && ++buf == SF_BUFS) {
+            buf = 0;
+            buf_phase ^= 1;
+          }
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
@@ -483,7 +566,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
         if (aborted) break;
         if (elect_one()) commit<CG>(&tfull[acc]);
         __syncwarp();
-        if (++acc == 2) {
+        if (++acc == C::ACCS) {
           acc = 0;
           acc_phase ^= 1;
         }
@@ -498,6 +581,89 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
       }
     }
     __syncwarp();
+  } else if (C::MX && warp == 10) {
+    // ======================= MXFP8 scales: batches of SF_KB k-blocks, all of A's rows of this CTA and of B's of the
+    // tile (a pair: both CTAs need all of B's). A lane reads the SF_KB words (k-blocks) of rows l, l + 32, l + 64,
+    // l + 96 of a block of 128 and writes, per k-block, these rows' words as the 16 bytes l of its chunk. The next
+    // batch is read before the wait for the buffer.
+    if constexpr (C::MX) {
+      uint32_t v[C::SF_BLOCKS][4][SF_KB];
+      Walk look(p, (int)blockIdx.x / CG, (int)gridDim.x / CG);
+      Seg s = look.next(p);
+      Origin o{};
+      int kb = 0, end = 0;  // next batch: k-blocks kb to the batch's end, of s
+      const auto start = [&] {
+        if (s.tile < 0) return;
+        o = origin<OP, CG, BN>(p, s.tile, rank);
+        kb = s.kb0 / SF_KB * SF_KB;
+        end = s.kb0 + s.nkb;
+      };
+      const auto fetch = [&] {
+#pragma unroll
+        for (int b = 0; b < C::SF_BLOCKS; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 128 * b + 32 * i + lane, n = r - BM;
+            const uint8_t* src = nullptr;
+            if (b == 0) {
+              if (r < o.rows) src = p.sfa + (o.m0 + r) * p.ld_sf;
+            } else if (C::GATEUP) {
+              const int c = n % (BN / 2);
+              if (c < o.cols) src = (n < BN / 2 ? p.sfb0 : p.sfb1) + (long long)(o.n0 + c) * p.ld_sf;
+            } else if (n < o.cols) {
+              src = p.sfb0 + (long long)(o.n0 + n) * p.ld_sf;
+            }
+            if (p.sf16) {
+              const uint4 w = src ? *reinterpret_cast<const uint4*>(src + 4 * kb) : make_uint4(0, 0, 0, 0);
+              v[b][i][0] = w.x;
+              v[b][i][1] = w.y;
+              v[b][i][2] = w.z;
+              v[b][i][3] = w.w;
+            } else {
+#pragma unroll
+              for (int k = 0; k < SF_KB; ++k)
+                v[b][i][k] = src && kb + k < p.KB ? reinterpret_cast<const uint32_t*>(src)[kb + k] : 0;
+            }
+          }
+      };
+      int buf = 0;
+      uint32_t phase = 0;
+      start();
+      while (s.tile >= 0) {
+        fetch();
+        if (!mbar_wait_warp(&sempty[buf], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) {
+          aborted = true;
+          break;
+        }
+        uint8_t* dst = sf_ring + buf * C::SF_BATCH_BYTES + 16 * lane;
+#pragma unroll
+        for (int k = 0; k < SF_KB; ++k)
+#pragma unroll
+          for (int b = 0; b < C::SF_BLOCKS; ++b)
+            *reinterpret_cast<uint4*>(dst + (k * C::SF_BLOCKS + b) * 512) =
+                make_uint4(v[b][0][k], v[b][1][k], v[b][2][k], v[b][3][k]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_first<CG>(&sfull[buf]);
+        if (++buf == SF_BUFS) {
+          buf = 0;
+          phase ^= 1;
+        }
+        kb += SF_KB;
+        if (kb >= end) {
+          s = look.next(p);
+          start();
+        }
+      }
+      // as the producer: until every batch is released
+      for (int i = 0; CG == 2 && i < SF_BUFS && !aborted; ++i) {
+        if (!mbar_wait_warp(&sempty[buf], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) aborted = true;
+        if (++buf == SF_BUFS) {
+          buf = 0;
+          phase ^= 1;
+        }
+      }
+    }
   } else {
     // ======================= epilogue: lane quadrant q, column half h
     const int ew = warp - 2, q = warp & 3, h = ew >> 2;
@@ -512,6 +678,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
       tc_fence_after();
       const Origin o = origin<OP, CG, BN>(p, s.tile, rank);
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN;
+      bool released = false;
       const int rows = o.rows - 32 * q;  // of this warp's 32 (may be <= 0)
       const long long row0 = (long long)o.m0 + 32 * q;
       if (s.slot >= 0) {
@@ -551,6 +718,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
           for (int i = 0; i < 32; ++i) g[i] = swiglu::act(g[i], u[i]);
           pack32(g, w);
           store_rows(stg, w, p.C + row0 * p.ldc + o.n0 + c, p.ldc, rows, cols);
+        }
+      } else if constexpr (C::MX) {
+        // one accumulator (BN = 256): released as soon as its columns are in registers, so the next tile's MMAs run
+        // beside what follows
+        constexpr int NB = BN / 64;  // blocks of 32 columns of this warp: gate then up
+        float v[NB][32];
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          tmem_ld32(tb + (C::GATEUP ? h * (BN / 4) + (j < NB / 2 ? 32 * j : BN / 2 + 32 * (j - NB / 2))
+                                    : h * (BN / 2) + 32 * j),
+                    v[j]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_first<CG>(&tempty[acc]);
+        released = true;
+        if constexpr (C::GATEUP) {
+#pragma unroll
+          for (int j = 0; j < NB / 2; ++j) {
+            const int c = h * (BN / 4) + 32 * j, cols = o.cols - c;
+            float am = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              v[j][i] = swiglu::act(v[j][i], v[j + NB / 2][i]);
+              am = fmaxf(am, fabsf(v[j][i]));
+            }
+            const uint8_t sb = ggmx::mx_scale_byte(am);
+            uint32_t w[8];
+            ggmx::quant32(v[j], ggmx::mx_inv_scale(sb), w);
+            store_rows8(stg, w, reinterpret_cast<uint8_t*>(p.C) + row0 * p.ldc + o.n0 + c, p.ldc, rows, cols);
+            if (lane < rows && cols > 0) p.C_sf[((row0 + lane) * p.ldc + o.n0 + c) >> 5] = sb;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            const int c = h * (BN / 2) + 32 * j;
+            uint32_t w[16];
+            pack32(v[j], w);
+            store_rows(stg, w, p.C + row0 * p.ldc + o.n0 + c, p.ldc, rows, o.cols - c);
+          }
         }
       } else if constexpr (OP == OP_DGRAD_ACT) {
 #pragma unroll 1
@@ -595,10 +802,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
           store_rows(stg, w, base + c, p.ldc, rows, cols);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_first<CG>(&tempty[acc]);
-      if (++acc == 2) {
+      if (!released) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_first<CG>(&tempty[acc]);
+      }
+      if (++acc == C::ACCS) {
         acc = 0;
         acc_phase ^= 1;
       }
@@ -608,7 +817,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
   if (CG == 2) pair_sync();  // everything the pair sends each other has arrived
   if (warp == 1) {
     tc_fence_after();
-    free_tmem<CG>(tmem_base, 2 * BN);
+    free_tmem<CG>(tmem_base, C::TMEM_COLS);
   }
 }
 
@@ -619,8 +828,12 @@ constexpr int FIX_THREADS = 256;
 constexpr int MAX_PIECES = 16, MANY_PIECES = 6;
 template <int OP, int CG, int BN, int SPLIT>
 __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constant__ Params p) {
-  constexpr int NV = OP == OP_GATEUP ? 16 : 8, FIX_ITEMS = FIX_THREADS / SPLIT;
+  constexpr bool GATEUP = is_gateup(OP), QUANT = OP == OP_GATEUP_MX;
+  constexpr int NV = GATEUP ? 16 : 8, FIX_ITEMS = FIX_THREADS / SPLIT;
   __shared__ float sums[SPLIT > 1 ? SPLIT - 1 : 1][NV][FIX_ITEMS];
+  // the activation to be quantised: rows in groups of FIX_ROWS, four items to a 1x32 block
+  constexpr int FIX_ROWS = FIX_ITEMS / 4;
+  __shared__ float amax[4][FIX_ROWS];
   griddep_wait();
   griddep_launch_dependents();
   const int i = blockIdx.x / CG, rank = CG == 2 ? (int)blockIdx.x & 1 : 0;
@@ -629,13 +842,17 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
   const Origin o = origin<OP, CG, BN>(p, p.n_full + i, rank);
   if (o.rows <= 0) return;
   const int part = threadIdx.x / FIX_ITEMS, item = threadIdx.x % FIX_ITEMS;
-  const int total = (o.cols + 7) / 8 * o.rows;
+  const int groups = (o.rows + FIX_ROWS - 1) / FIX_ROWS;
+  const int total = QUANT ? groups * (o.cols / 32) * FIX_ITEMS : (o.cols + 7) / 8 * o.rows;
   for (int e0 = blockIdx.y * FIX_ITEMS; e0 < total; e0 += gridDim.y * FIX_ITEMS) {  // the same for the whole CTA
-    const int e = e0 + item, r = e % o.rows, c = 8 * (e / o.rows);
+    const int e = e0 + item, g = e0 / FIX_ITEMS;
+    const int r = QUANT ? g % groups * FIX_ROWS + item % FIX_ROWS : e % o.rows;
+    const int c = QUANT ? g / groups * 32 + item / FIX_ROWS * 8 : 8 * (e / o.rows);
+    const bool ok = e < total && r < o.rows;
     float v[8], u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
-    if (e < total) {
+    if (ok) {
 #pragma unroll 4
       for (int b = b0 + part; b <= b1; b += SPLIT) {
         const int slot = 2 * b + (b * p.sk_per > i * p.KB ? 0 : 1);
@@ -643,7 +860,7 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           v[j] += src[j * BM];
-          if (OP == OP_GATEUP) u[j] += src[(BN / 2 + j) * BM];
+          if (GATEUP) u[j] += src[(BN / 2 + j) * BM];
         }
       }
     }
@@ -653,7 +870,7 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           sums[part - 1][j][item] = v[j];
-          if (OP == OP_GATEUP) sums[part - 1][(NV - 8) + j][item] = u[j];
+          if (GATEUP) sums[part - 1][(NV - 8) + j][item] = u[j];
         }
       __syncthreads();
       if (part == 0)
@@ -662,11 +879,38 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             v[j] += sums[s][j][item];
-            if (OP == OP_GATEUP) u[j] += sums[s][(NV - 8) + j][item];
+            if (GATEUP) u[j] += sums[s][(NV - 8) + j][item];
           }
     }
-    if (part > 0 || e >= total) continue;
     const long long row = o.m0 + r;
+    if constexpr (QUANT) {
+      float am = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = swiglu::act(v[j], u[j]);
+        am = fmaxf(am, fabsf(v[j]));
+      }
+      __syncthreads();  // the last round's have been read
+      if (part == 0) amax[item / FIX_ROWS][item % FIX_ROWS] = am;
+      __syncthreads();
+      if (part > 0 || !ok) continue;
+      const int l = item % FIX_ROWS;
+      const uint8_t sb = ggmx::mx_scale_byte(fmaxf(fmaxf(amax[0][l], amax[1][l]), fmaxf(amax[2][l], amax[3][l])));
+      const float inv = ggmx::mx_inv_scale(sb);
+      uint32_t w[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        w[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * k] * inv, v[4 * k + 1] * inv), __NV_SATFINITE,
+                                                  __NV_E4M3) |
+               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * k + 2] * inv, v[4 * k + 3] * inv), __NV_SATFINITE,
+                                                  __NV_E4M3)
+                   << 16;
+      const long long at = row * p.ldc + o.n0 + c;
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p.C) + at) = make_uint2(w[0], w[1]);
+      if (item / FIX_ROWS == 0) p.C_sf[at >> 5] = sb;
+      continue;
+    }
+    if (part > 0 || !ok) continue;
     const auto pack = [](const float (&t)[8]) {
       return make_uint4(pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3]), pack_bf16x2(t[4], t[5]),
                         pack_bf16x2(t[6], t[7]));
@@ -748,7 +992,7 @@ int max_pairs() {
   if (!cached[dev]) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2 * (MAX_CTAS / 2));
-    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.blockDim = dim3(Cfg<OP, 2, 256>::THREADS);
     cfg.dynamicSmemBytes = Cfg<OP, 2, 256>::SMEM_BYTES;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -793,7 +1037,7 @@ Plan plan(Params& p) {
     if (workers == 0) continue;
     const int per = (p.M + BM * cg - 1) / (BM * cg), tiles_m = p.halves * per;
     for (int bn = 128; bn <= 256; bn *= 2) {
-      const int step = OP == OP_GATEUP ? bn / 2 : bn;
+      const int step = is_gateup(OP) ? bn / 2 : bn;
       const int tiles_n = (p.N + step - 1) / step;
       const long long total = (long long)tiles_m * tiles_n, rounds = total / workers;
       const int rest = (int)(total % workers);
@@ -802,7 +1046,7 @@ Plan plan(Params& p) {
       const bool cut = rest && split < whole;
       if (std::min(whole, split) >= best) continue;
       best = std::min(whole, split);
-      c = {cg, bn, workers, OP == OP_GATEUP ? bn / 2 : std::min(128, bn / cg)};
+      c = {cg, bn, workers, is_gateup(OP) ? bn / 2 : std::min(128, bn / cg)};
       p.tiles_m = tiles_m;
       p.tm_split = per;
       p.tiles_n = tiles_n;
@@ -823,7 +1067,7 @@ int launch_form(const Params& p, int workers, cudaStream_t st, bool dep) {
     return MOE_ERR_CUDA;
   }
   const int n = p.sk_tiles || p.n_full > workers ? workers : p.n_full;
-  int rc = launch_dep(kern, dim3(n * CG), NUM_THREADS, C::SMEM_BYTES, CG, st, p, dep);
+  int rc = launch_dep(kern, dim3(n * CG), C::THREADS, C::SMEM_BYTES, CG, st, p, dep);
   if (rc || !p.sk_tiles) return rc;
   const int per_tile = BM * C::N_STEP / 8 / FIX_THREADS;  // CTAs, one item per thread
   if (p.KB > MANY_PIECES * p.sk_per)

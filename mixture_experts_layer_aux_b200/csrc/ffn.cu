@@ -3,8 +3,7 @@
 // MXFP8 and backward in bf16.
 //   few tokens    the streaming kernels of stream.cuh (two launches; MXFP8 from
 //                 a bf16 x: three);
-//   more, bf16    the dense tensor-core kernel of dense.cuh;
-//   more, MXFP8   the block-scaled grouped GEMM as one group.
+//   more          the dense tensor-core kernel of dense.cuh.
 // Backward: dgrad of the down projection with the SwiGLU backward in its
 // epilogue, the weight gradients, and dX = dgate W_g + dup W_u as one product
 // over [dgate | dup].
@@ -12,14 +11,6 @@
 #include "dense.cuh"
 #include "layout.h"
 #include "stream.cuh"
-
-namespace moe_impl {
-int gemm_gateup_mx(int rows, int groups, int H, int F, const void* A, const uint8_t* A_sf, const void* Wg,
-                   const uint8_t* Wg_sf, const void* Wu, const uint8_t* Wu_sf, const int32_t* offsets,
-                   const float* row_gate, void* C, uint8_t* C_sf, void* save, cudaStream_t st);
-int gemm_down_mx(int rows, int groups, int H, int F, const void* A, const uint8_t* A_sf, const void* Wd,
-                 const uint8_t* Wd_sf, const int32_t* offsets, void* C, cudaStream_t st);
-}  // namespace moe_impl
 
 namespace ffn {
 
@@ -136,7 +127,6 @@ struct FwdWs {
   float* part;
   Padded pad;
   uint8_t *xq, *xq_sf, *aq, *aq_sf;
-  int32_t* off;
 };
 static size_t carve_fwd(void* ws, const moe_ffn_config* c, FwdWs* w) {
   Carve cv(ws);
@@ -147,7 +137,7 @@ static size_t carve_fwd(void* ws, const moe_ffn_config* c, FwdWs* w) {
     w->xq_sf = cv.take<uint8_t>(T * H / 32);
     w->aq = cv.take<uint8_t>(T * F);
     w->aq_sf = cv.take<uint8_t>(T * F / 32);
-    w->off = cv.take<int32_t>(2);
+    if (c->T > STREAM_T) w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
   } else {
     if (!c->save_for_bwd) w->a = cv.take<__nv_bfloat16>(T * pad64(c->F));
     if (c->T > STREAM_T) w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
@@ -338,20 +328,37 @@ static int fwd_bf16(const moe_ffn_config* c, const void* x, const void* Wg, cons
   return down(T, H, F, a, md, y, w.part, st, true);
 }
 
+// One product in MXFP8: out [T, N] = x W0^T, or the activation of x W0^T and x W1^T with its scales.
+template <int OP>
+static int dense_mx(int T, int N, int K, const void* x, const uint8_t* x_sf, const void* W0, const uint8_t* sf0,
+                    const void* W1, const uint8_t* sf1, void* out, uint8_t* out_sf, float* part, cudaStream_t st,
+                    bool dep) {
+  Params p = base_params(T, N, K / 128, part, out, N);
+  const dense::Plan c = dense::plan<OP>(p);
+  const auto map = [&](CUtensorMap* m, const void* a, int rows, int box) {
+    return moe_host::encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, a, K, rows, K, 128, box);
+  };
+  if (!map(&p.tmA, x, T, 128) || !map(&p.tmB0, W0, N, c.b_box) || (W1 && !map(&p.tmB1, W1, N, c.b_box)))
+    return MOE_ERR_CUDA;
+  p.sfa = x_sf;
+  p.sfb0 = sf0;
+  p.sfb1 = sf1;
+  p.ld_sf = K / 32;
+  p.sf16 = K % 512 == 0 && a16(x_sf) && a16(sf0) && a16(sf1);
+  p.C_sf = out_sf;
+  return dense::launch<OP>(p, c, st, dep);
+}
+
 static int fwd_mxfp8(const moe_ffn_config* c, const void* x, const uint8_t* x_sf, const void* Wg, const void* Wu,
                      const void* Wd, const uint8_t* Wg_sf, const uint8_t* Wu_sf, const uint8_t* Wd_sf, void* y,
                      const FwdWs& w, cudaStream_t st) {
   const int T = c->T, H = c->H, F = c->F;
   const bool quant = x_sf == nullptr;
   if (quant) {
-    if (T <= STREAM_T) {
-      const long long n8 = (long long)T * H / 8;
-      quantize_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), n8, w.xq,
-                                                                   w.xq_sf);
-      MOE_CHECK_LAUNCH();
-    } else {
-      FFN_RC(moe_impl::quantize_mxfp8(x, T, H, w.xq, w.xq_sf, st));
-    }
+    const long long n8 = (long long)T * H / 8;
+    quantize_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), n8, w.xq,
+                                                                 w.xq_sf);
+    MOE_CHECK_LAUNCH();
     x = w.xq;
     x_sf = w.xq_sf;
   }
@@ -361,10 +368,8 @@ static int fwd_mxfp8(const moe_ffn_config* c, const void* x, const uint8_t* x_sf
     return stream_gemm<true, false>(T, H, F, Wd, nullptr, Wd_sf, nullptr, Mat{w.aq, F}, w.aq_sf, y, H, nullptr,
                                     Saved{}, st, true);
   }
-  FFN_RC(moe_impl::fill_offsets2(w.off, T, st));
-  FFN_RC(moe_impl::gemm_gateup_mx(T, 1, H, F, x, x_sf, Wg, Wg_sf, Wu, Wu_sf, w.off, nullptr, w.aq, w.aq_sf, nullptr,
-                                  st));
-  return moe_impl::gemm_down_mx(T, 1, H, F, w.aq, w.aq_sf, Wd, Wd_sf, w.off, y, st);
+  FFN_RC((dense_mx<dense::OP_GATEUP_MX>(T, F, H, x, x_sf, Wg, Wg_sf, Wu, Wu_sf, w.aq, w.aq_sf, w.part, st, quant)));
+  return dense_mx<dense::OP_DOWN_MX>(T, H, F, w.aq, w.aq_sf, Wd, Wd_sf, nullptr, nullptr, y, nullptr, w.part, st, true);
 }
 
 }  // namespace ffn
