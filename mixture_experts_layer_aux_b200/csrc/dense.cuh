@@ -4,6 +4,8 @@
 //   down      y   = a W_d^T
 //   dgrad     dgu = SwiGLU backward of (dY W_d),  dX = dgate W_g + dup W_u
 //   wgrad     dW  = dO^T act
+// and the first two in MXFP8 (K % 128 == 0), with the scales of both operands
+// copied to TMEM beside the accumulators.
 // Everything past an edge of M, N or K is zero-filled by TMA on the way in and
 // predicated on the way out, so no operand is padded.
 //
@@ -19,11 +21,12 @@
 // w % 4, column half). Every wait is bounded (MOE_WAIT_NS).
 //
 // Work split. Whole tiles go round robin over the CTAs (pairs) while they fill
-// every SM; a rest that would leave many idle for long is one line of k-blocks
-// instead, cut into equal pieces, one per CTA (pair). A piece that holds a
-// whole tile is finished in place; the others leave fp32 partial accumulators
-// in the workspace (at most two per CTA), and fixup_kernel adds them in the
-// order of K and applies the epilogue, so results do not depend on timing.
+// every SM. The tiles of a rest that would leave many idle for long are cut
+// along K, into one piece per CTA (pair) where that can be, else as one line of
+// k-blocks in equal pieces. Pieces leave fp32 partial accumulators in the
+// workspace (at most two per CTA; a piece that holds a whole tile finishes it),
+// and fixup_kernel adds them in the order of K and applies the epilogue, so
+// results do not depend on timing.
 #pragma once
 
 #include <algorithm>
@@ -42,7 +45,7 @@ constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int STG_ROW = 80;  // staging: 32 rows x (64 + 16) bytes per epilogue warp
 constexpr int STG_BYTES = EPI_WARPS * 32 * STG_ROW;
 constexpr int BAR_BYTES = 256;
-constexpr int SF_KB = 4, SF_BUFS = 3;  // MXFP8: k-blocks in a batch of scales, batches in shared memory
+constexpr int SF_KB = 4;  // MXFP8: k-blocks whose scales are read at once
 constexpr int MAX_CTAS = 160;                            // CTAs of one launch (one per SM)
 constexpr size_t SLOT_FLOATS = (size_t)BM * MAX_BN;          // one CTA's partial accumulator
 constexpr size_t PART_BYTES = 2ull * MAX_CTAS * SLOT_FLOATS * sizeof(float);
@@ -70,6 +73,7 @@ struct __align__(64) Params {
   int n_full;          // tiles done whole, round robin
   int sk_tiles;        // tiles n_full .. n_full + sk_tiles - 1, cut along K
   int sk_per;          // k-blocks per CTA (pair) of those
+  int sk_kb;           // length of a tile on their line, >= KB: a multiple of sk_per where pieces end with their tile
   float* part;
   __nv_bfloat16* C;
   __nv_bfloat16* C2;
@@ -99,7 +103,7 @@ struct Seg {
 struct Walk {
   int w, u, end, t, step;
   MOE_DEV Walk(const Params& p, int w_, int n) {
-    const int units = p.sk_tiles * p.KB;
+    const int units = p.sk_tiles * p.sk_kb;
     w = w_;
     u = min(w * p.sk_per, units);
     end = min(u + p.sk_per, units);
@@ -109,12 +113,12 @@ struct Walk {
   MOE_DEV Seg next(const Params& p) {
     Seg s;
     if (u < end) {
-      const int i = u / p.KB;
-      s.kb0 = u - i * p.KB;
+      const int i = u / p.sk_kb;
+      s.kb0 = u - i * p.sk_kb;  // < KB: no piece starts in the gap behind a tile
       s.nkb = min(p.KB - s.kb0, end - u);
       s.tile = p.n_full + i;
       s.slot = s.nkb == p.KB ? -1 : 2 * w + (s.kb0 > 0 ? 0 : 1);
-      u += s.nkb;
+      u = p.sk_kb > p.KB ? end : u + s.nkb;
       return s;
     }
     s.kb0 = 0;
@@ -134,12 +138,12 @@ struct Cfg {
   static constexpr bool MX = is_mx(OP), GATEUP = is_gateup(OP);
   static constexpr int N_STEP = GATEUP ? BN / 2 : BN;           // output columns per tile
   static constexpr int B_ROWS = BN / CG;                        // of B, per CTA
-  static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK * 2;
-  static constexpr int kStages = (BN == 128 ? (CG == 2 ? 8 : 6) : CG == 2 ? 6 : 4) - (MX ? 1 : 0);
+  static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK * 2;  // by TMA
+  static constexpr int kStages = BN == 128 ? (CG == 2 ? 8 : 6) : CG == 2 ? 6 : 4;
   static constexpr int THREADS = NUM_THREADS + (MX ? 32 : 0);   // MXFP8: one warp for the scales
   static constexpr int SF_BLOCKS = (BM + BN) / 128;             // MXFP8: 512-byte scale chunks of a k-block
-  static constexpr int SF_BATCH_BYTES = MX ? SF_KB * SF_BLOCKS * 512 : 0;
-  static constexpr int SMEM_BYTES = 1024 + kStages * STAGE_BYTES + SF_BUFS * SF_BATCH_BYTES + STG_BYTES + BAR_BYTES;
+  static constexpr int SF_BYTES = MX ? SF_BLOCKS * 512 : 0;
+  static constexpr int SMEM_BYTES = 1024 + kStages * (STAGE_BYTES + SF_BYTES) + STG_BYTES + BAR_BYTES;
   static constexpr int B_BOX = GATEUP ? BN / 2 : B_ROWS < 128 ? B_ROWS : 128;  // rows of a K-major B box
   // TMEM: accumulators, then two slots of scales (4 columns per chunk)
   static constexpr int ACCS = MX && BN == 256 ? 1 : 2;
@@ -234,12 +238,6 @@ MOE_DEV void commit(uint64_t* bar) {
                    : "memory");
   }
 }
-// mbar_wait_warp on a barrier that ordinary writes of the pair's other CTA are behind.
-MOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int code) {
-  if (!mbar_wait_warp(bar, parity, abort, status, code)) return false;
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  return true;
-}
 // Arrives on the first CTA's barrier.
 template <int CG>
 MOE_DEV void arrive_first(uint64_t* bar) {
@@ -247,6 +245,17 @@ MOE_DEV void arrive_first(uint64_t* bar) {
     mbar_arrive(bar);
   else
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(pair_addr(smem_u32(bar), 0))
+                 : "memory");
+}
+// The same after writes to this CTA's own shared memory that only this SM's tensor core reads: the proxy fence before it
+// has made them visible there, and a release at the cluster's scope would wait for the warp's reads of global memory
+// and more (0.9 us per k-block where 0.35 is the MMAs').
+template <int CG>
+MOE_DEV void arrive_first_relaxed(uint64_t* bar) {
+  if constexpr (CG == 1)
+    mbar_arrive(bar);
+  else
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(pair_addr(smem_u32(bar), 0))
                  : "memory");
 }
 template <int CG>
@@ -375,31 +384,25 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sf_ring = smem + kStages * C::STAGE_BYTES;
-  uint8_t* stg_area = sf_ring + SF_BUFS * C::SF_BATCH_BYTES;
+  uint8_t* stg_area = sf_ring + kStages * C::SF_BYTES;
   uint64_t* full = reinterpret_cast<uint64_t*>(stg_area + STG_BYTES);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint64_t* sfull = drain + 1;
-  uint64_t* sempty = sfull + SF_BUFS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + SF_BUFS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)blockIdx.x & 1 : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], C::MX ? 1 + CG : 1);  // the producer, and the loaders of scales
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], CG * EPI_WARPS);
-    }
-    for (int i = 0; C::MX && i < SF_BUFS; ++i) {
-      mbar_init(&sfull[i], CG);
-      mbar_init(&sempty[i], 1);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -503,8 +506,7 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
       constexpr uint32_t IDESC = idesc_bf16(CG * BM, BN, C::A_MN ? 1 : 0, C::B_MN ? 1 : 0);
       const uint64_t sd0 = C::MX ? ggmx::sf_desc(smem_u32(sf_ring)) : 0;
       const uint32_t sf_tmem = tmem_base + C::ACCS * BN;
-      int buf = 0, slot = 0;
-      uint32_t buf_phase = 0;
+      int slot = 0;
       constexpr int A_STEP = (C::A_MN ? 2048 : 32) >> 4, B_STEP = (C::B_MN ? 2048 : 32) >> 4;  // 16 of K
       const uint32_t base = smem_u32(smem);
       const uint64_t a0 = smem_desc_sw128(base, C::A_MN ? 64 * BK * 2 : 16, 1024);
@@ -523,28 +525,19 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
             aborted = true;
             break;
           }
-          const int in_batch = (s.kb0 + kb) % SF_KB;
-          if (C::MX && (kb == 0 || in_batch == 0)) {
-            if (!mbar_wait_cluster(&sfull[buf], buf_phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
-              aborted = true;
-              break;
-            }
-          }
           tc_fence_after();
-          const bool sf_done = C::MX && (in_batch == SF_KB - 1 || kb == s.nkb - 1);
           if (elect_one()) {
             const uint64_t ad = a0 + stage * (C::STAGE_BYTES >> 4), bd = b0 + stage * (C::STAGE_BYTES >> 4);
             if constexpr (C::MX) {
               // slots alternate: the copies into one follow, in issue order, the MMAs that read it two k-blocks ago
               const uint32_t sc = sf_tmem + slot * 4 * C::SF_BLOCKS;
-              const uint64_t sd = sd0 + ((buf * C::SF_BATCH_BYTES + in_batch * C::SF_BLOCKS * 512) >> 4);
+              const uint64_t sd = sd0 + stage * (C::SF_BYTES >> 4);
 #pragma unroll
               for (int i = 0; i < C::SF_BLOCKS; ++i) copy_sf<CG>(sc + 4 * i, sd + i * (512 >> 4));
 #pragma unroll
               for (int q = 0; q < 4; ++q)
                 mma_mx<CG>(d_tmem, ad + 2 * q, bd + 2 * q, ggmx::idesc_mx(CG * BM, BN, q), sc | ((uint32_t)q << 30),
                            (sc + 4) | ((uint32_t)q << 30), (kb | q) != 0 ? 1u : 0u);
-              if (sf_done) commit<CG>(&sempty[buf]);
             } else {
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk)
@@ -554,10 +547,6 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
           }
           __syncwarp();
           slot ^= 1;
-          if (sf_done && ++buf == SF_BUFS) {
-            buf = 0;
-            buf_phase ^= 1;
-          }
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
@@ -582,23 +571,17 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
     }
     __syncwarp();
   } else if (C::MX && warp == 10) {
-    // ======================= MXFP8 scales: batches of SF_KB k-blocks, all of A's rows of this CTA and of B's of the
-    // tile (a pair: both CTAs need all of B's). A lane reads the SF_KB words (k-blocks) of rows l, l + 32, l + 64,
-    // l + 96 of a block of 128 and writes, per k-block, these rows' words as the 16 bytes l of its chunk. The next
-    // batch is read before the wait for the buffer.
+    // ======================= MXFP8 scales, of A's rows of this CTA and of all of B's of the tile (a pair: each CTA
+    // needs all). They join their stage: the loader waits for the stage as the producer does, and arrives on its
+    // barrier. A lane reads the words of SF_KB k-blocks of rows l, l + 32, l + 64, l + 96 of a block of 128, one batch
+    // ahead, and writes, per k-block, these rows' words as the 16 bytes l of its chunk; one proxy fence for two
+    // k-blocks.
     if constexpr (C::MX) {
-      uint32_t v[C::SF_BLOCKS][4][SF_KB];
-      Walk look(p, (int)blockIdx.x / CG, (int)gridDim.x / CG);
-      Seg s = look.next(p);
-      Origin o{};
-      int kb = 0, end = 0;  // next batch: k-blocks kb to the batch's end, of s
-      const auto start = [&] {
-        if (s.tile < 0) return;
-        o = origin<OP, CG, BN>(p, s.tile, rank);
-        kb = s.kb0 / SF_KB * SF_KB;
-        end = s.kb0 + s.nkb;
-      };
+      uint32_t cur[C::SF_BLOCKS][4][SF_KB], nxt[C::SF_BLOCKS][4][SF_KB];
+      Seg s = walk.next(p);
+      int base = s.kb0 / SF_KB * SF_KB;  // the batch in nxt: k-blocks base .. base + SF_KB - 1 of s
       const auto fetch = [&] {
+        const Origin o = origin<OP, CG, BN>(p, s.tile, rank);
 #pragma unroll
         for (int b = 0; b < C::SF_BLOCKS; ++b)
 #pragma unroll
@@ -614,53 +597,62 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
               src = p.sfb0 + (long long)(o.n0 + n) * p.ld_sf;
             }
             if (p.sf16) {
-              const uint4 w = src ? *reinterpret_cast<const uint4*>(src + 4 * kb) : make_uint4(0, 0, 0, 0);
-              v[b][i][0] = w.x;
-              v[b][i][1] = w.y;
-              v[b][i][2] = w.z;
-              v[b][i][3] = w.w;
+              const uint4 w = src ? *reinterpret_cast<const uint4*>(src + 4 * base) : make_uint4(0, 0, 0, 0);
+              nxt[b][i][0] = w.x;
+              nxt[b][i][1] = w.y;
+              nxt[b][i][2] = w.z;
+              nxt[b][i][3] = w.w;
             } else {
 #pragma unroll
               for (int k = 0; k < SF_KB; ++k)
-                v[b][i][k] = src && kb + k < p.KB ? reinterpret_cast<const uint32_t*>(src)[kb + k] : 0;
+                nxt[b][i][k] = src && base + k < p.KB ? reinterpret_cast<const uint32_t*>(src)[base + k] : 0;
             }
           }
       };
-      int buf = 0;
+      int stage = 0;
       uint32_t phase = 0;
-      start();
-      while (s.tile >= 0) {
-        fetch();
-        if (!mbar_wait_warp(&sempty[buf], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) {
-          aborted = true;
-          break;
-        }
-        uint8_t* dst = sf_ring + buf * C::SF_BATCH_BYTES + 16 * lane;
+      if (s.tile >= 0) fetch();
+      while (s.tile >= 0 && !aborted) {
+        const int k0 = max(s.kb0 - base, 0), k1 = min(s.kb0 + s.nkb - base, SF_KB);  // the batch's k-blocks
 #pragma unroll
-        for (int k = 0; k < SF_KB; ++k)
+        for (int b = 0; b < C::SF_BLOCKS; ++b)
 #pragma unroll
-          for (int b = 0; b < C::SF_BLOCKS; ++b)
-            *reinterpret_cast<uint4*>(dst + (k * C::SF_BLOCKS + b) * 512) =
-                make_uint4(v[b][0][k], v[b][1][k], v[b][2][k], v[b][3][k]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_first<CG>(&sfull[buf]);
-        if (++buf == SF_BUFS) {
-          buf = 0;
-          phase ^= 1;
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < SF_KB; ++k) cur[b][i][k] = nxt[b][i][k];
+        base += SF_KB;
+        if (base >= s.kb0 + s.nkb) {
+          s = walk.next(p);
+          base = s.kb0 / SF_KB * SF_KB;
         }
-        kb += SF_KB;
-        if (kb >= end) {
-          s = look.next(p);
-          start();
-        }
-      }
-      // as the producer: until every batch is released
-      for (int i = 0; CG == 2 && i < SF_BUFS && !aborted; ++i) {
-        if (!mbar_wait_warp(&sempty[buf], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) aborted = true;
-        if (++buf == SF_BUFS) {
-          buf = 0;
-          phase ^= 1;
+        if (s.tile >= 0) fetch();
+#pragma unroll
+        for (int k = 0; k < SF_KB; k += 2) {
+          int st[2] = {-1, -1};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (k + j < k0 || k + j >= k1 || aborted) continue;
+            if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) {
+              aborted = true;
+              continue;
+            }
+            uint8_t* dst = sf_ring + stage * C::SF_BYTES + 16 * lane;
+#pragma unroll
+            for (int b = 0; b < C::SF_BLOCKS; ++b)
+              *reinterpret_cast<uint4*>(dst + b * 512) =
+                  make_uint4(cur[b][0][k + j], cur[b][1][k + j], cur[b][2][k + j], cur[b][3][k + j]);
+            st[j] = stage;
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (st[0] >= 0) arrive_first_relaxed<CG>(&full[st[0]]);
+            if (st[1] >= 0) arrive_first_relaxed<CG>(&full[st[1]]);
+          }
         }
       }
     }
@@ -837,7 +829,8 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
   griddep_wait();
   griddep_launch_dependents();
   const int i = blockIdx.x / CG, rank = CG == 2 ? (int)blockIdx.x & 1 : 0;
-  const int b0 = (int)((long long)i * p.KB / p.sk_per), b1 = (int)(((long long)(i + 1) * p.KB - 1) / p.sk_per);
+  const int b0 = (int)((long long)i * p.sk_kb / p.sk_per);
+  const int b1 = (int)(((long long)i * p.sk_kb + p.KB - 1) / p.sk_per);
   if (b0 == b1) return;  // one CTA (pair) held the whole tile and finished it
   const Origin o = origin<OP, CG, BN>(p, p.n_full + i, rank);
   if (o.rows <= 0) return;
@@ -855,7 +848,7 @@ __global__ void __launch_bounds__(FIX_THREADS) fixup_kernel(const __grid_constan
     if (ok) {
 #pragma unroll 4
       for (int b = b0 + part; b <= b1; b += SPLIT) {
-        const int slot = 2 * b + (b * p.sk_per > i * p.KB ? 0 : 1);
+        const int slot = 2 * b + (b * p.sk_per > i * p.sk_kb ? 0 : 1);
         const float* src = p.part + (size_t)(slot * CG + rank) * SLOT_FLOATS + (size_t)c * BM + r;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -1021,12 +1014,16 @@ struct Plan {
 
 // The form of least estimated time: rounds of tiles times k-blocks times a k-block's time, measured in us (down
 // projection, T = H = F = 4096, all in one launch: 97.9 us with one CTA and 256 columns, 109.0 with 128, pairs 82.1 and
-// 91.2; 24 k-blocks of T = 1001, H = 2048: 14.4, 11.6, 14.4 and 12.3). Cutting the tiles of the last round along K
-// saves the idle part of that round and costs partial sums out and in again and one more kernel, 6 to 10 us with 128
-// columns, 10 to 19 with 256 (T = 333, H = 2048, F = 5504 with 128: 24.6 us whole, 18.5 cut; T = 700: 25.0 and 26.7).
+// 91.2, MXFP8 57.9, 71.3, 57.4 and 71.7; 24 k-blocks of T = 1001, H = 2048: 14.4, 11.6, 14.4 and 12.3). Cutting the
+// tiles of the last round along K saves the idle part of that round and costs partial sums out and in again and one
+// more kernel: 5 us and about 1.2 per piece of a tile where every CTA has one piece (T = 128, H = 4096, F = 14336, one
+// CTA and 128 columns: 55.8 us whole, 38.9 in 2 pieces, 34.8 in 3, 32.6 in 4; 256 columns 87.9, 54.1, 45.3, 39.0, 34.9
+// in 8). A rest of more than half a round cannot be cut so; there the line of its k-blocks is cut into equal pieces,
+// of which most CTAs have two (13 us).
 template <int OP>
 Plan plan(Params& p) {
-  static constexpr float KB_US[2][2] = {{0.22f, 0.355f}, {0.185f, 0.29f}};  // [pairs][256 columns]
+  static constexpr float KB_US[2][2][2] = {{{0.22f, 0.355f}, {0.185f, 0.29f}},   // bf16: [pairs][256 columns]
+                                           {{0.285f, 0.395f}, {0.29f, 0.38f}}};  // MXFP8
   int sms = moe_host::num_sms();
   if (sms > MAX_CTAS) sms = MAX_CTAS;
   const int pairs = std::min(max_pairs<OP>(), sms / 2);
@@ -1041,18 +1038,28 @@ Plan plan(Params& p) {
       const int tiles_n = (p.N + step - 1) / step;
       const long long total = (long long)tiles_m * tiles_n, rounds = total / workers;
       const int rest = (int)(total % workers);
-      const float tile = p.KB * KB_US[cg - 1][bn / 256], cost = bn == 256 ? 12.f : 9.f;
-      const float whole = (rounds + (rest ? 1 : 0)) * tile, split = (rounds + (float)rest / workers) * tile + cost;
-      const bool cut = rest && split < whole;
-      if (std::min(whole, split) >= best) continue;
-      best = std::min(whole, split);
-      c = {cg, bn, workers, is_gateup(OP) ? bn / 2 : std::min(128, bn / cg)};
-      p.tiles_m = tiles_m;
-      p.tm_split = per;
-      p.tiles_n = tiles_n;
-      p.n_full = (int)(cut ? total - rest : total);
-      p.sk_tiles = cut ? rest : 0;
-      p.sk_per = cut ? std::max((rest * p.KB + workers - 1) / workers, (p.KB + MAX_PIECES - 1) / MAX_PIECES) : 0;
+      const float kb = KB_US[is_mx(OP)][cg - 1][bn / 256];
+      const auto take = [&](float us, int cut, int sk_per, int sk_kb) {
+        if (us >= best) return;
+        best = us;
+        c = {cg, bn, workers, is_gateup(OP) ? bn / 2 : std::min(128, bn / cg)};
+        p.tiles_m = tiles_m;
+        p.tm_split = per;
+        p.tiles_n = tiles_n;
+        p.n_full = (int)(total - cut);
+        p.sk_tiles = cut;
+        p.sk_per = sk_per;
+        p.sk_kb = sk_kb;
+      };
+      take((rounds + (rest ? 1 : 0)) * p.KB * kb, 0, 0, p.KB);
+      for (int n = 2; rest > 0 && n <= MAX_PIECES && rest * n <= workers && n <= p.KB; ++n) {
+        const int len = (p.KB + n - 1) / n, used = (p.KB + len - 1) / len;  // pieces of a tile, none empty
+        take((rounds * p.KB + len) * kb + 5.f + 1.2f * used, rest, len, len * used);
+      }
+      if (2 * rest > workers) {
+        const int len = (rest * p.KB + workers - 1) / workers;
+        take((rounds * p.KB + len) * kb + 13.f, rest, len, p.KB);
+      }
     }
   }
   return c;
@@ -1066,7 +1073,8 @@ int launch_form(const Params& p, int workers, cudaStream_t st, bool dep) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }
-  const int n = p.sk_tiles || p.n_full > workers ? workers : p.n_full;
+  int n = std::min(p.n_full, workers);
+  if (p.sk_tiles) n = std::max(n, (p.sk_tiles * p.sk_kb + p.sk_per - 1) / p.sk_per);
   int rc = launch_dep(kern, dim3(n * CG), C::THREADS, C::SMEM_BYTES, CG, st, p, dep);
   if (rc || !p.sk_tiles) return rc;
   const int per_tile = BM * C::N_STEP / 8 / FIX_THREADS;  // CTAs, one item per thread

@@ -118,7 +118,7 @@ def test_backward_parts(moe):
 
 MX_SHAPES = [(1, 256, 128), (5, 4096, 512), (48, 4096, 640), (64, 2048, 1280), (1, 7168, 2048), (5, 512, 384), (8, 256, 640), (12, 768, 256), (20, 1024, 512),
              (33, 768, 4096), (64, 512, 256), (65, 512, 256), (7, 256, 19072), (50, 256, 9600), (3, 19200, 128),
-             (130, 768, 640), (700, 1024, 384)]
+             (130, 768, 640), (700, 1024, 384), (2100, 512, 4224), (1300, 4352, 640)]
 
 
 def mx_of(moe, w):
