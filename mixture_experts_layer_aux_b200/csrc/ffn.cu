@@ -16,8 +16,11 @@ namespace ffn {
 
 using dense::Params;
 
-// Tokens up to which the streaming kernels are taken.
-constexpr int STREAM_T = stream::MAX_T;
+// Tokens up to which the streaming kernels are taken. MXFP8: their loader fetches the scales by the word, the dense
+// kernel's by four (H = 7168, F = 2048: 16 tokens 26.9 us streaming and 30.6 dense, 32 tokens 31.0 and 28.0; H = 4096,
+// F = 14336: 8 tokens 57.7 and 57.2, 32 tokens 62.0 and 49.4).
+constexpr int STREAM_T = stream::MAX_T, STREAM_T_MX = 16;
+static bool streams(const moe_ffn_config* c) { return c->T <= (c->dtype == MOE_DT_MXFP8 ? STREAM_T_MX : STREAM_T); }
 
 #define FFN_RC(x)         \
   do {                    \
@@ -137,10 +140,10 @@ static size_t carve_fwd(void* ws, const moe_ffn_config* c, FwdWs* w) {
     w->xq_sf = cv.take<uint8_t>(T * H / 32);
     w->aq = cv.take<uint8_t>(T * F);
     w->aq_sf = cv.take<uint8_t>(T * F / 32);
-    if (c->T > STREAM_T) w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
+    if (!streams(c)) w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
   } else {
     if (!c->save_for_bwd) w->a = cv.take<__nv_bfloat16>(T * pad64(c->F));
-    if (c->T > STREAM_T) w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
+    if (!streams(c)) w->part = cv.take<float>(dense::PART_BYTES / sizeof(float));
     w->pad = carve_padded(cv, c, false);
   }
   return cv.used;
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __nv_bfloat16* __re
 static int fwd_bf16(const moe_ffn_config* c, const void* x, const void* Wg, const void* Wu, const void* Wd, void* y,
                     __nv_bfloat16* a, const Saved& s, const FwdWs& w, cudaStream_t st) {
   const int T = c->T, H = c->H, F = c->F, Fp = pad64(F);
-  if (T <= STREAM_T) {
+  if (streams(c)) {
     FFN_RC((stream_gemm<false, true>(T, F, H, Wg, Wu, nullptr, nullptr, Mat{x, H}, nullptr, a, Fp, nullptr, s, st,
                                      false, Wd)));
     return stream_gemm<false, false>(T, H, F, Wd, nullptr, nullptr, nullptr, Mat{a, Fp}, nullptr, y, H, nullptr,
@@ -362,7 +365,7 @@ static int fwd_mxfp8(const moe_ffn_config* c, const void* x, const uint8_t* x_sf
     x = w.xq;
     x_sf = w.xq_sf;
   }
-  if (T <= STREAM_T) {
+  if (streams(c)) {
     FFN_RC((stream_gemm<true, true>(T, F, H, Wg, Wu, Wg_sf, Wu_sf, Mat{x, H}, x_sf, w.aq, F, w.aq_sf, Saved{}, st,
                                     quant, Wd)));
     return stream_gemm<true, false>(T, H, F, Wd, nullptr, Wd_sf, nullptr, Mat{w.aq, F}, w.aq_sf, y, H, nullptr,

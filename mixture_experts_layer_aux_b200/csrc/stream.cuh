@@ -33,9 +33,8 @@
 // for the down kernel's to be brought into L2, so that memory stays busy while
 // the one ends and the other begins.
 //
-// Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer and TMEM owner
-// (where one is too slow, warp 3 is a second issuer; the rings then have an even
-// number of stages, so that a stage has one issuer, who sees all its phases), warp 2 loader of the MXFP8 scales (natural [rows, K/32] layout -> the chunk
+// Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer and TMEM owner,
+// warp 2 loader of the MXFP8 scales (natural [rows, K/32] layout -> the chunk
 // order of the tensor-memory copies, see gemm_mx.cuh), warps 4..11 epilogue
 // (TMEM lane quadrant w % 4, every other 16 tokens). Every wait is bounded
 // (MOE_WAIT_NS).
@@ -59,16 +58,11 @@ constexpr int MAX_T = 64;
 constexpr int MAX_STAGES = 16;
 constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
 constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-// MMA issuers, each with accumulators of its own and every other stage: one thread's instructions (some 35 ns an MMA,
-// 60 a copy of scales or a commit) keep up with memory at the two large operands of bf16 gate/up, not at 14 KB of
-// down weights per stage, or at MXFP8 with its scales (8 tokens, H = 7168, F = 2048: 28.7 us with one, 26.8 with
-// two).
-constexpr int issuers(bool mx, bool gateup) { return mx || !gateup ? 2 : 1; }
 // Kernels whose tiles may be shared by a cluster.
 constexpr bool clusters(bool mx, bool gateup) { return mx || !gateup; }
 constexpr int ROW_BYTES = 128;            // K bytes of a stage row (64 bf16 or 128 e4m3)
 constexpr int OPERAND_BYTES = 128 * ROW_BYTES;  // what an MMA reads of its weight operand, filled or not
-constexpr int MAX_N = 224;                // s T at most (two issuers' accumulators and the scales in 512 TMEM columns)
+constexpr int MAX_N = 224;                // s T at most (two accumulators and the scales in 512 TMEM columns)
 constexpr int SF_SLOTS = 16;              // MXFP8: stages of scales in shared memory, on a ring of their own
 constexpr int SF_SLOT_COLS = 16;          // scale columns of a stage in TMEM (W0, W1: 128 rows; x: 256 rows)
 constexpr int MAX_PARTS = 9;              // K blocks of a stage, at most 8 (4 with MXFP8), and the tail
@@ -117,7 +111,6 @@ struct __align__(64) Params {
   int* status;
 };
 
-static_assert(SF_SLOTS % 2 == 0, "a slot of scales has one issuer");
 
 // Instruction descriptors: bf16 (common.cuh) and MXFP8 (gemm_mx.cuh) with a run-time N.
 template <bool MX>
@@ -197,7 +190,6 @@ MOE_DEV void save_preact(const Params& p, int tok, int col, float g, float u) {
 
 template <bool MX, bool GATEUP>
 __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_constant__ Params p) {
-  constexpr int ISSUERS = issuers(MX, GATEUP);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* tail = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = tail + p.tail_bytes;
@@ -211,7 +203,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
   uint64_t* tempty = tfull + 2;
   uint64_t* tail_full = tempty + 2;
   uint64_t* drain = tail_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + ISSUERS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w_bytes = p.w_rows * ROW_BYTES;
@@ -233,11 +225,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
       mbar_init(&sempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&tfull[i], ISSUERS);
+      mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], EPI_WARPS);
     }
     mbar_init(tail_full, 1);
-    for (int i = 0; i < ISSUERS; ++i) mbar_init(&drain[i], 1);
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -331,14 +323,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
         }
     }
     __syncwarp();
-  } else if (warp == 1 || (ISSUERS == 2 && warp == 3)) {
-    // ======================= MMA issuers. Descriptors are those of the first stage plus the address / 16.
-    const int me = warp >> 1;
+  } else if (warp == 1) {
+    // ======================= MMA issuer. Descriptors are those of the first stage plus the address / 16.
     const bool two = GATEUP && !p.merged;
     const uint64_t desc0 = smem_desc_sw128(smem_u32(ring), 16, 1024);
     const uint64_t sdesc0 = ggmx::sf_desc(smem_u32(sf_ring));
     const uint32_t stage16 = p.stage_bytes >> 4, w16 = w_bytes >> 4, x16 = x_off >> 4;
-    const uint32_t sf_tmem = tmem_base + p.acc_bufs * ISSUERS * p.acc_cols + me * 2 * SF_SLOT_COLS;
+    const uint32_t sf_tmem = tmem_base + p.acc_bufs * p.acc_cols;
     uint32_t id[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) id[q] = idesc<MX>(p.mma_n, q);
@@ -360,13 +351,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
         break;
       }
       tc_fence_after();
-      const uint32_t d0 = tmem_base + (acc * ISSUERS + me) * p.acc_cols, d1 = d0 + p.mma_n;
+      const uint32_t d0 = tmem_base + acc * p.acc_cols, d1 = d0 + p.mma_n;
       bool first = true, slot2 = false;
       for (int ks = ks0; ks < ks1; ++ks) {
-        if (ISSUERS == 2 && (stage & 1) != me) {  // the other issuer's
-          step();
-          continue;
-        }
         if ((MX && !mbar_wait_warp(&sfull[slot], sphase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) ||
             !mbar_wait_warp(&full[stage], phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
           aborted = true;
@@ -413,7 +400,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
         step();
       }
       if (aborted) break;
-      if (with_tail && me == 0) {
+      if (with_tail) {
         // into accumulators of its own: its operands' rows are not stacked
         if (!mbar_wait_warp(tail_full, 0, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
           aborted = true;
@@ -423,7 +410,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
         if (elect_one()) {
           const uint64_t at = smem_desc_sw128(smem_u32(tail), 16, 1024), wt = p.r8 * ROW_BYTES >> 4;
           const uint64_t bt = at + (GATEUP ? 2 : 1) * wt;
-          const uint32_t dt = tmem_base + p.acc_bufs * ISSUERS * p.acc_cols, idt = idesc<MX>(p.tail_n, 0);
+          const uint32_t dt = tmem_base + p.acc_bufs * p.acc_cols, idt = idesc<MX>(p.tail_n, 0);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             mma_bf16(dt, at + 2 * q, bt + 2 * q, idt, q != 0 ? 1u : 0u);
@@ -441,10 +428,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
     }
     if (*abort_flag) {
       // wait for every MMA already issued before TMEM is released
-      if (elect_one()) mma_commit(&drain[me]);
+      if (elect_one()) mma_commit(drain);
       __syncwarp();
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(&drain[me], 0) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
+      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < MOE_WAIT_NS) {
       }
     }
     __syncwarp();
@@ -531,7 +518,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
     griddep_wait();  // what the kernel before this one still reads may be what is written here
     const int q = warp & 3, h = (warp - EPI_WARP0) >> 2;
     const int row = 32 * q + lane;
-    int acc = 0, iter = 0;
+    int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = tile0; t < p.tiles && !aborted; t += tile_step) {
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_EPILOGUE))) {
@@ -539,37 +526,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
         break;
       }
       tc_fence_after();
-      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + acc * ISSUERS * p.acc_cols;
-      const uint32_t tail_tb = tmem_base + ((uint32_t)(q * 32) << 16) + p.acc_bufs * ISSUERS * p.acc_cols;
-      // with a single stage of K, only its issuer's accumulator holds something
-      const bool both = ISSUERS == 2 && ks1 - ks0 > 1;
-      const uint32_t tb1 = ISSUERS == 1 || both || !(iter++ & 1) ? tb : tb + p.acc_cols;
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + acc * p.acc_cols;
+      const uint32_t tail_tb = tmem_base + ((uint32_t)(q * 32) << 16) + p.acc_bufs * p.acc_cols;
       const int n0 = t * p.r;
       const int rows = min(p.r, p.N - n0);
       if (p.staged) break;  // one tile per CTA, finished below
       const bool ok = row < rows;
       for (int c = 16 * h; c < p.T; c += 32) {
         float v[16], u[16], v2[16], u2[16];
-        tmem_ld16(tb1 + c, v);
-        if (GATEUP) tmem_ld16(tb1 + p.mma_n + c, u);
-        if (both) {
-          tmem_ld16(tb + p.acc_cols + c, v2);
-          if (GATEUP) tmem_ld16(tb + p.acc_cols + p.mma_n + c, u2);
-        }
+        tmem_ld16(tb + c, v);
+        if (GATEUP) tmem_ld16(tb + p.mma_n + c, u);
         tmem_ld_wait();
-        const auto add = [&] {
+        if (with_tail) {
+          tmem_ld16(tail_tb + c, v2);
+          if (GATEUP) tmem_ld16(tail_tb + p.tail_n + c, u2);
+          tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             v[i] += v2[i];
             if (GATEUP) u[i] += u2[i];
           }
-        };
-        if (both) add();
-        if (with_tail) {
-          tmem_ld16(tail_tb + c, v2);
-          if (GATEUP) tmem_ld16(tail_tb + p.tail_n + c, u2);
-          tmem_ld_wait();
-          add();
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -618,20 +594,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
       tc_fence_after();
       const int q = warp & 3, h = (warp - EPI_WARP0) >> 2, row = 32 * q + lane;
       const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16);
-      const bool both = ISSUERS == 2 && ks1 - ks0 > 1;
       for (int op = 0; op < ops; ++op) {
         for (int j = 16 * h; j < p.s * p.T; j += 32) {
           float v[16];
           tmem_ld16(tq + op * p.mma_n + j, v);
-          if (both) {
-            float v2[16];
-            tmem_ld16(tq + p.acc_cols + op * p.mma_n + j, v2);
-            tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] += v2[k];
-          } else {
-            tmem_ld_wait();
-          }
+          tmem_ld_wait();
           if (!CLUSTER || cs == 1) {
             float* dst = reinterpret_cast<float*>(ring) + ((size_t)op * cols + j) * 128 + row;
 #pragma unroll
@@ -655,7 +622,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
         if (with_tail) {
           for (int j = 16 * h; j < p.T; j += 32) {
             float v[16];
-            tmem_ld16(tq + ISSUERS * p.acc_cols + op * p.tail_n + j, v);
+            tmem_ld16(tq + p.acc_cols + op * p.tail_n + j, v);
             tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -720,7 +687,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
 // (boxes of 128 bytes x r rows, or T tokens, x s blocks).
 template <bool MX, bool GATEUP>
 Params plan(int T, int N, int K) {
-  constexpr int ISSUERS = issuers(MX, GATEUP);
   Params p{};
   p.T = T;
   p.N = N;
@@ -760,7 +726,7 @@ Params plan(int T, int N, int K) {
       const int rows = (s * p.r + 7) / 8 * 8, n = (s * T + 15) / 16 * 16, ops = GATEUP && !merged ? 2 : 1;
       if (rows * (merged ? 2 : 1) > 128 || (s > 1 && (s * T > MAX_N || s > p.KB))) continue;
       const int stage = (GATEUP ? 2 : 1) * rows * ROW_BYTES + n * ROW_BYTES;
-      const int cols = ISSUERS * ops * n + (MX ? 2 * ISSUERS * SF_SLOT_COLS : 16) + (p.tail ? ops * p.tail_n : 0);
+      const int cols = ops * n + (MX ? 2 * SF_SLOT_COLS : 16) + (p.tail ? ops * p.tail_n : 0);
       if (s > 1 && (cols > 512 || 4 * stage > RING_ALONE - (MX ? SF_SLOTS * 2048 : 40 * 1024))) continue;
       // a staged epilogue's accumulators fit where the ring (four stages at least) was
       if ((s > 1 || merged) && 512 * ops * (s * (T + MAX_CLUSTER - 1) + (p.tail ? T + 1 : 0)) > 4 * stage) continue;
@@ -788,15 +754,14 @@ Params plan(int T, int N, int K) {
   p.stages = ((GATEUP ? RING_GATEUP : RING_DOWN) - used) / p.stage_bytes;
   if (p.stages < 4 || all > SHORT_BYTES) p.stages = (RING_ALONE - used) / p.stage_bytes;
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
-  p.stages -= p.stages % ISSUERS;
   const int reach = (GATEUP && !p.merged ? p.w_rows * ROW_BYTES : 0) + OPERAND_BYTES;  // of the operands of a stage
   p.ring_bytes = p.stages * p.stage_bytes + (reach > p.stage_bytes ? reach - p.stage_bytes : 0);
   p.acc_cols = (GATEUP && !p.merged ? 2 : 1) * p.mma_n;
   // past the accumulators: the scales, or the tail's, or what a last read may pass them by
-  const int more = MX ? 2 * ISSUERS * SF_SLOT_COLS
+  const int more = MX ? 2 * SF_SLOT_COLS
                       : p.tail ? (GATEUP && !p.merged ? 2 : 1) * p.tail_n + 16 : p.s > 1 ? 16 : 0;
-  p.acc_bufs = one || 2 * ISSUERS * p.acc_cols + more > 512 ? 1 : 2;
-  const int cols = p.acc_bufs * ISSUERS * p.acc_cols + more;
+  p.acc_bufs = one || 2 * p.acc_cols + more > 512 ? 1 : 2;
+  const int cols = p.acc_bufs * p.acc_cols + more;
   p.tmem_cols = 32;
   while (p.tmem_cols < cols) p.tmem_cols *= 2;
   p.status = moe_host::device_status_ptr();
