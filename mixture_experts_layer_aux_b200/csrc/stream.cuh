@@ -594,31 +594,43 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
       tc_fence_after();
       const int q = warp & 3, h = (warp - EPI_WARP0) >> 2, row = 32 * q + lane;
       const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16);
-      for (int op = 0; op < ops; ++op) {
-        for (int j = 16 * h; j < p.s * p.T; j += 32) {
-          float v[16];
-          tmem_ld16(tq + op * p.mma_n + j, v);
-          tmem_ld_wait();
-          if (!CLUSTER || cs == 1) {
-            float* dst = reinterpret_cast<float*>(ring) + ((size_t)op * cols + j) * 128 + row;
+      // block c of K is in rows [c r, (c + 1) r) and columns [c T, (c + 1) T): the columns that this warp's rows need
+      int e0 = 32 * q, e1 = e0 + 31;
+      if (p.merged && e0 >= p.w_rows) {  // rows of W_u
+        e0 -= p.w_rows;
+        e1 -= p.w_rows;
+      } else if (p.merged && e1 >= p.w_rows) {
+        e0 = 0;
+        e1 = p.w_rows;
+      }
+      const int j0 = min(e0 / p.r, p.s - 1) * p.T, j1 = (min(e1 / p.r, p.s - 1) + 1) * p.T;
+      const int chunks = e0 < p.s * p.r ? (j1 - j0 + 15) >> 4 : 0;
+      for (int i = h; i < ops * chunks; i += 2) {
+        const int op = i >= chunks, j = j0 + 16 * (i - op * chunks);
+        float v[16];
+        tmem_ld16(tq + op * p.mma_n + j, v);
+        tmem_ld_wait();
+        if (!CLUSTER || cs == 1) {
+          float* dst = reinterpret_cast<float*>(ring) + ((size_t)op * cols + j) * 128 + row;
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (j + k < cols) dst[128 * k] = v[k];
-          } else {
-            int c = j / p.T, tok = j - c * p.T;
+          for (int k = 0; k < 16; ++k)
+            if (j + k < j1) dst[128 * k] = v[k];
+        } else {
+          int c = j / p.T, tok = j - c * p.T;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              if (c < p.s) {
-                const uint32_t at = ((uint32_t)((rank * ops + op) * cols + c * Tl + (tok >> lc)) * 128 + row) * 4;
-                st_cluster(cluster_addr(smem_u32(ring), tok & (cs - 1)) + at, v[k]);
-              }
-              if (++tok == p.T) {
-                tok = 0;
-                ++c;
-              }
+          for (int k = 0; k < 16; ++k) {
+            if (j + k < j1) {
+              const uint32_t at = ((uint32_t)((rank * ops + op) * cols + c * Tl + (tok >> lc)) * 128 + row) * 4;
+              st_cluster(cluster_addr(smem_u32(ring), tok & (cs - 1)) + at, v[k]);
+            }
+            if (++tok == p.T) {
+              tok = 0;
+              ++c;
             }
           }
         }
+      }
+      for (int op = 0; op < ops; ++op) {
         if (with_tail) {
           for (int j = 16 * h; j < p.T; j += 32) {
             float v[16];
