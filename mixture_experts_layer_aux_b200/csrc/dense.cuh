@@ -238,20 +238,12 @@ MOE_DEV void commit(uint64_t* bar) {
                    : "memory");
   }
 }
-// Arrives on the first CTA's barrier.
+// Arrives on the first CTA's barrier. What the arrival stands for is done by then: accumulators are in registers
+// (tcgen05.wait::ld), and scales in this SM's shared memory, for its tensor core to read (proxy fence). A release at the
+// cluster's scope would also wait for every access to global memory in flight: 1 us per tile, and 0.9 us per k-block
+// of MXFP8, whose MMAs take 0.35.
 template <int CG>
 MOE_DEV void arrive_first(uint64_t* bar) {
-  if constexpr (CG == 1)
-    mbar_arrive(bar);
-  else
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(pair_addr(smem_u32(bar), 0))
-                 : "memory");
-}
-// The same after writes to this CTA's own shared memory that only this SM's tensor core reads: the proxy fence before it
-// has made them visible there, and a release at the cluster's scope would wait for the warp's reads of global memory
-// and more (0.9 us per k-block where 0.35 is the MMAs').
-template <int CG>
-MOE_DEV void arrive_first_relaxed(uint64_t* bar) {
   if constexpr (CG == 1)
     mbar_arrive(bar);
   else
@@ -650,8 +642,8 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (st[0] >= 0) arrive_first_relaxed<CG>(&full[st[0]]);
-            if (st[1] >= 0) arrive_first_relaxed<CG>(&full[st[1]]);
+            if (st[0] >= 0) arrive_first<CG>(&full[st[0]]);
+            if (st[1] >= 0) arrive_first<CG>(&full[st[1]]);
           }
         }
       }
