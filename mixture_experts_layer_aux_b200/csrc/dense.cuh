@@ -70,6 +70,7 @@ struct __align__(64) Params {
   int halves;          // OP_WGRAD: 2 for two stacked outputs of M rows each (A2, C2 the second), else 1
   int tiles_m, tiles_n;
   int tm_split;        // m-tiles of one half
+  int n_fast, group;   // order of the tiles: n before m, and how many of the faster one before the slower moves on
   int n_full;          // tiles done whole, round robin
   int sk_tiles;        // tiles n_full .. n_full + sk_tiles - 1, cut along K
   int sk_per;          // k-blocks per CTA (pair) of those
@@ -160,8 +161,11 @@ struct Origin {
 template <int OP, int CG, int BN>
 MOE_DEV Origin origin(const Params& p, int tile, int rank) {
   Origin o;
-  const int mt = tile % p.tiles_m;  // m fastest: the CTAs of a wave share a few column panels of B
-  const int nt = tile / p.tiles_m;
+  // the tiles of p.group rows (or columns) by turns, along all columns (rows)
+  const int fast = p.n_fast ? p.tiles_n : p.tiles_m, slow = p.n_fast ? p.tiles_m : p.tiles_n;
+  const int g = tile / (p.group * slow), i = tile - g * p.group * slow, w = min(p.group, fast - g * p.group);
+  const int ft = g * p.group + i % w, st = i / w;
+  const int mt = p.n_fast ? st : ft, nt = p.n_fast ? ft : st;
   o.second = OP == OP_WGRAD && mt >= p.tm_split;
   o.m0 = (mt - (o.second ? p.tm_split : 0)) * BM * CG + rank * BM;
   o.n0 = nt * Cfg<OP, CG, BN>::N_STEP;
@@ -1004,6 +1008,13 @@ struct Plan {
   int b_box;    // rows of a K-major B box
 };
 
+// Order of the tiles: the smaller operand stays in L2 while the other streams by; one too large for that goes in groups
+// of panels (T = 16384, H = 4096, F = 14336, the block's forward: 5400 us m first, 4900 the smaller first, 4290 in
+// groups; MXFP8, H = F = 8192: 3315, 3175, 2865; a training step of T = 4096: 3550, 3310 and, with everything in
+// groups, 3380).
+constexpr long long L2_KEEP = 48ll << 20;
+constexpr int GROUP_ROWS = 2048;
+
 // The form of least estimated time: rounds of tiles times k-blocks times a k-block's time, measured in us (down
 // projection, T = H = F = 4096, all in one launch: 97.9 us with one CTA and 256 columns, 109.0 with 128, pairs 82.1 and
 // 91.2, MXFP8 57.9, 71.3, 57.4 and 71.7; 24 k-blocks of T = 1001, H = 2048: 14.4, 11.6, 14.4 and 12.3). Cutting the
@@ -1054,6 +1065,10 @@ Plan plan(Params& p) {
       }
     }
   }
+  const long long rows_a = (long long)p.M * p.halves, rows_b = (long long)p.N * (is_gateup(OP) ? 2 : 1);
+  p.n_fast = rows_b < rows_a;
+  const int fast = p.n_fast ? p.tiles_n : p.tiles_m;
+  p.group = std::min(rows_a, rows_b) * p.KB * 128 > L2_KEEP ? std::min(fast, GROUP_ROWS / (BM * c.cg)) : fast;
   return c;
 }
 
