@@ -459,8 +459,9 @@ int moe_rmsnorm_bwd(int32_t T, int32_t H, const void* dY, const void* h, const v
  *     4-byte aligned.
  *   NVFP4: MOE_ERR_UNSUPPORTED.
  *   y [T,H] bf16, not overlapping the inputs. saved: moe_ffn_saved_size()
- *   bytes when save_for_bwd (else NULL): the bf16 gate and up pre-activations
- *   and the activation.
+ *   bytes when save_for_bwd (else NULL): the gate and up pre-activations cut to
+ *   24 bits (16 of significand) and the bf16 activation, in a layout of their
+ *   own.
  *   T <= 2^24; H, F <= 2^20.
  *
  * moe_ffn_bwd: the derivative for upstream dY [T,H] bf16 (BF16, save_for_bwd
