@@ -19,8 +19,9 @@ using dense::Params;
 // Tokens up to which the streaming kernels are taken. MXFP8: their loader fetches the scales by the word, the dense
 // kernel's by four (H = 7168, F = 2048: 16 tokens 26.9 us streaming and 30.6 dense, 32 tokens 31.0 and 28.0; H = 4096,
 // F = 14336: 8 tokens 57.7 and 57.2, 32 tokens 62.0 and 49.4).
-constexpr int STREAM_T = stream::MAX_T, STREAM_T_MX = 16;
-static bool streams(const moe_ffn_config* c) { return c->T <= (c->dtype == MOE_DT_MXFP8 ? STREAM_T_MX : STREAM_T); }
+static bool streams(const moe_ffn_config* c) {
+  return c->T <= (c->dtype == MOE_DT_MXFP8 ? stream::MAX_T_MX : stream::MAX_T);
+}
 
 #define FFN_RC(x)         \
   do {                    \

@@ -54,7 +54,7 @@ bool encode_tmap_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, ui
 
 namespace stream {
 
-constexpr int MAX_T = 64;
+constexpr int MAX_T = 64, MAX_T_MX = 16;
 constexpr int MAX_STAGES = 16;
 constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
 constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
@@ -63,8 +63,11 @@ constexpr bool clusters(bool mx, bool gateup) { return mx || !gateup; }
 constexpr int ROW_BYTES = 128;            // K bytes of a stage row (64 bf16 or 128 e4m3)
 constexpr int OPERAND_BYTES = 128 * ROW_BYTES;  // what an MMA reads of its weight operand, filled or not
 constexpr int MAX_N = 224;                // s T at most (two accumulators and the scales in 512 TMEM columns)
-constexpr int SF_SLOTS = 16;              // MXFP8: stages of scales in shared memory, on a ring of their own
-constexpr int SF_SLOT_COLS = 16;          // scale columns of a stage in TMEM (W0, W1: 128 rows; x: 256 rows)
+// MXFP8: stages of scales in shared memory, and how many the loader asks for ahead of the one it hands over. It has then
+// waited for the operands' stage, so the slot of SF_SLOTS stages before is free where the ring has no more than
+// SF_SLOTS - SF_AHEAD stages.
+constexpr int SF_SLOTS = 16, SF_AHEAD = 8;
+constexpr int SF_SLOT_COLS = 12;          // scale columns of a stage in TMEM (W0, W1, x: 128 rows each)
 constexpr int MAX_PARTS = 9;              // K blocks of a stage, at most 8 (4 with MXFP8), and the tail
 constexpr int MAX_CLUSTER = 4;            // CTAs that share a tile, each taking a part of K
 constexpr int BAR_BYTES = 1024;
@@ -164,11 +167,12 @@ MOE_DEV void cp_async4(void* smem_dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(bytes)
                : "memory");
 }
-// Arrives on `bar` (counted among its expected arrivals) once this thread's copies so far have landed.
-MOE_DEV void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+MOE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last N groups have landed.
+template <int N>
+MOE_DEV void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-MOE_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Where an operand row's scale word lies in its chunks.
 MOE_DEV int chunk_offset(int row) { return 512 * (row >> 7) + 16 * (row & 31) + 4 * ((row >> 5) & 3); }
@@ -197,9 +201,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
   uint8_t* bar_area = sf_ring + (MX ? SF_SLOTS * p.sf_bytes : 0);
   uint64_t* full = reinterpret_cast<uint64_t*>(bar_area);
   uint64_t* empty = full + MAX_STAGES;
-  uint64_t* sfull = empty + MAX_STAGES;
-  uint64_t* sempty = sfull + SF_SLOTS;
-  uint64_t* tfull = sempty + SF_SLOTS;
+  uint64_t* tfull = empty + MAX_STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* tail_full = tempty + 2;
   uint64_t* drain = tail_full + 1;
@@ -217,12 +219,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], MX ? 2 : 1);  // the producer, and the loader of scales
       mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; MX && i < SF_SLOTS; ++i) {
-      mbar_init(&sfull[i], 32);  // the loader's lanes
-      mbar_init(&sempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
@@ -334,12 +332,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
 #pragma unroll
     for (int q = 0; q < 4; ++q) id[q] = idesc<MX>(p.mma_n, q);
     int stage = 0, slot = 0, acc = 0;
-    uint32_t phase = 0, sphase = 0, acc_phase = 0;
+    uint32_t phase = 0, acc_phase = 0;
     const auto step = [&] {
-      if (MX && ++slot == SF_SLOTS) {
-        slot = 0;
-        sphase ^= 1;
-      }
+      if (MX && ++slot == SF_SLOTS) slot = 0;
       if (++stage == p.stages) {
         stage = 0;
         phase ^= 1;
@@ -354,13 +349,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
       const uint32_t d0 = tmem_base + acc * p.acc_cols, d1 = d0 + p.mma_n;
       bool first = true, slot2 = false;
       for (int ks = ks0; ks < ks1; ++ks) {
-        if ((MX && !mbar_wait_warp(&sfull[slot], sphase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) ||
-            !mbar_wait_warp(&full[stage], phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
+        if (!mbar_wait_warp(&full[stage], phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
           aborted = true;
           break;
         }
         tc_fence_after();
-        if (MX) fence_proxy_async_smem();  // the scales were written by ordinary copies, and are read by tcgen05.cp
         if (elect_one()) {
           const uint64_t ad = desc0 + stage * stage16, bd = ad + x16;
           // scale slots of TMEM alternate: the copies of a stage follow, in issue order, the MMAs that read the slot
@@ -371,7 +364,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
             ggmx::tmem_cp_32x128b_x4(sc, sd);
             if (two) ggmx::tmem_cp_32x128b_x4(sc + 4, sd + (512 >> 4));
             ggmx::tmem_cp_32x128b_x4(sc + 8, sx);
-            if (p.mma_n > 128) ggmx::tmem_cp_32x128b_x4(sc + 12, sx + (512 >> 4));
           }
           const auto mma = [&](uint32_t d, uint64_t a, uint32_t sa, int q) {
             const uint32_t on = !first || q != 0 ? 1u : 0u;
@@ -392,7 +384,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
             for (int q = 0; q < 4; ++q) mma(d0, ad, sc, q);
           }
           mma_commit(&empty[stage]);
-          if (MX) mma_commit(&sempty[slot]);
         }
         __syncwarp();
         slot2 = !slot2;
@@ -438,14 +429,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
   } else if (warp == 2) {
     // ======================= MXFP8 scales. A chunk holds 128 operand rows: row 32 i + l in bytes 16 l + 4 i .. + 3,
     // one byte per 1x32 block of a K block. Every word goes from its place in the natural layout to its place in the
-    // chunk by a 4-byte asynchronous copy whose completion arrives on its slot's barrier. Sixteen stages of scales
-    // are in flight (through registers, with the next four K blocks loaded ahead, the loads' latency set the pace:
-    // 32.8 us for 29 MB of gate/up weights; as deep as the operands' ring only, 22.6).
+    // chunk by a 4-byte asynchronous copy, SF_AHEAD stages before it is needed (through registers, with the next four
+    // K blocks loaded ahead, the loads' latency set the pace). The scales then join the operands' stage: the loader
+    // waits for it as the producer does, and arrives on its barrier.
     if constexpr (MX) {
       const int kw = p.K / 32;  // scale bytes per row
       // Lane l copies the words of operand rows l + 32 j: block c = row / r of weight row (token) row % r. A block
       // past the end of K (of a last stage) or a row past the weights is zero-filled.
-      constexpr int WJ = 4, XJ = MAX_N / 32;
+      constexpr int WJ = 4, XJ = 4 * MAX_T_MX / 32;
       const uint8_t *w0[WJ], *xs[XJ];
       int wc[WJ], wd[WJ], xc[XJ];
       const long long w1 = GATEUP ? p.sf1 - p.sf0 : 0;
@@ -483,35 +474,55 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
         for (int j = 0; j < XJ; ++j) {
           if (lane + 32 * j >= p.s * p.T) continue;
           const bool ok = ks * p.s + xc[j] < p.KB;
-          cp_async4(sf + 512 * (j >> 2) + 16 * lane + 4 * (j & 3), ok ? xs[j] + 4 * ks * p.s : p.x_sf, ok ? 4 : 0);
+          cp_async4(sf + 16 * lane + 4 * j, ok ? xs[j] + 4 * ks * p.s : p.x_sf, ok ? 4 : 0);
         }
-        cp_async_arrive(&sfull[st]);
       };
-      // (a slot's arrival waits for every copy before it: not many stages ahead of the tokens' scales)
-      const int ahead = min(4, ks1 - ks0);
-      for (int st = 0; st < ahead; ++st) weights(ks0 + st, st);
+      // The next item to ask for: stage iks of tile it, into slot islot.
+      int it = tile0, iks = ks0, islot = 0;
+      const auto advance = [&] {
+        if (++islot == SF_SLOTS) islot = 0;
+        if (++iks == ks1) {
+          iks = ks0;
+          it += tile_step;
+          if (it < p.tiles) rows(it);
+        }
+      };
+      const int ahead = min(4, ks1 - ks0);  // the weights', before the wait for the tokens'
+      for (int j = 0; j < ahead; ++j) weights(ks0 + j, j);
       griddep_wait();
-      int slot = 0;
+      for (int j = 0; j < SF_AHEAD; ++j) {
+        if (it < p.tiles) {
+          if (j >= ahead) weights(iks, islot);
+          tokens(iks, islot);
+          advance();
+        }
+        cp_async_commit();
+      }
+      int stage = 0;
       uint32_t phase = 0;
       for (int t = tile0; t < p.tiles && !aborted; t += tile_step) {
-        if (t != tile0) rows(t);
         for (int ks = ks0; ks < ks1; ++ks) {
-          if (t != tile0 || ks >= ks0 + ahead) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&sempty[slot], phase ^ 1, abort_flag, p.status,
-                                                   DEV_WAIT_TIMEOUT_PRODUCER))) {
-              aborted = true;
-              break;
-            }
-            weights(ks, slot);
+          if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.status, DEV_WAIT_TIMEOUT_PRODUCER)) {
+            aborted = true;
+            break;
           }
-          tokens(ks, slot);
-          if (++slot == SF_SLOTS) {
-            slot = 0;
+          if (it < p.tiles) {
+            weights(iks, islot);
+            tokens(iks, islot);
+            advance();
+          }
+          cp_async_commit();
+          cp_async_wait<SF_AHEAD>();
+          fence_proxy_async_smem();  // written by ordinary copies, read by tcgen05.cp
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[stage]);
+          if (++stage == p.stages) {
+            stage = 0;
             phase ^= 1;
           }
         }
       }
-      cp_async_wait_all();  // (after an abort) no copy outlives the CTA
+      cp_async_wait<0>();  // (after an abort) no copy outlives the CTA
     }
   } else if (warp >= EPI_WARP0) {
     // ======================= epilogue: TMEM lanes 32 q .. 32 q + 31 = rows of the tile, columns = tokens
@@ -759,13 +770,13 @@ Params plan(int T, int N, int K) {
   p.stage_bytes = (GATEUP ? 2 : 1) * p.w_rows * ROW_BYTES + p.mma_n * ROW_BYTES;
   p.sf_w1 = p.merged ? 0 : 512;
   p.sf_x = GATEUP && !p.merged ? 1024 : 512;
-  p.sf_bytes = p.sf_x + (p.mma_n + 127) / 128 * 512;
+  p.sf_bytes = p.sf_x + 512;
   const int sf_ring = MX ? SF_SLOTS * p.sf_bytes : 0;
   const long long all = (long long)p.KS / p.cs * p.stage_bytes * ((p.tiles + sms - 1) / sms);
   const int used = sf_ring + p.tail_bytes;
   p.stages = ((GATEUP ? RING_GATEUP : RING_DOWN) - used) / p.stage_bytes;
   if (p.stages < 4 || all > SHORT_BYTES) p.stages = (RING_ALONE - used) / p.stage_bytes;
-  if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+  p.stages = std::min(p.stages, MX ? SF_SLOTS - SF_AHEAD : MAX_STAGES);
   const int reach = (GATEUP && !p.merged ? p.w_rows * ROW_BYTES : 0) + OPERAND_BYTES;  // of the operands of a stage
   p.ring_bytes = p.stages * p.stage_bytes + (reach > p.stage_bytes ? reach - p.stage_bytes : 0);
   p.acc_cols = (GATEUP && !p.merged ? 2 : 1) * p.mma_n;
