@@ -63,18 +63,19 @@ constexpr bool clusters(bool mx, bool gateup) { return mx || !gateup; }
 constexpr int ROW_BYTES = 128;            // K bytes of a stage row (64 bf16 or 128 e4m3)
 constexpr int OPERAND_BYTES = 128 * ROW_BYTES;  // what an MMA reads of its weight operand, filled or not
 constexpr int MAX_N = 224;                // s T at most (two accumulators and the scales in 512 TMEM columns)
-// MXFP8: stages of scales in shared memory, and how many the loader asks for ahead of the one it hands over. It has then
+// MXFP8: stages of scales in shared memory, and how many the loader asks for ahead of the one it hands over (8 tokens,
+// H = 7168, F = 2048: 24.4 us with 1, 23.2 with 2, 24.4 with 4, 24.9 with 8, whose first stage is late). It has then
 // waited for the operands' stage, so the slot of SF_SLOTS stages before is free where the ring has no more than
 // SF_SLOTS - SF_AHEAD stages.
-constexpr int SF_SLOTS = 16, SF_AHEAD = 8;
+constexpr int SF_SLOTS = 8, SF_AHEAD = 2;
 constexpr int SF_SLOT_COLS = 12;          // scale columns of a stage in TMEM (W0, W1, x: 128 rows each)
 constexpr int MAX_PARTS = 9;              // K blocks of a stage, at most 8 (4 with MXFP8), and the tail
 constexpr int MAX_CLUSTER = 4;            // CTAs that share a tile, each taking a part of K
 constexpr int BAR_BYTES = 1024;
 // Bytes of the ring. A CTA with little to stream (up to SHORT_BYTES in all) leaves room for one of the other kernel
 // on its SM, which then starts while it runs; with much to stream, bytes in flight count: about 2 us of latency at
-// 46 GB/s per SM (T = 1, H = 4096, F = 14336 bf16: 65 us with the large rings, 70 with the shared ones; MXFP8
-// H = 7168, F = 2048: 32.4 and 28.7).
+// 46 GB/s per SM (T = 1, H = 4096, F = 14336 bf16, with an earlier form of these kernels: 65 us with the large rings, 70
+// with the shared ones; MXFP8 H = 7168, F = 2048: 32.4 and 28.7).
 constexpr int RING_GATEUP = 116 * 1024, RING_DOWN = 100 * 1024, RING_ALONE = 200 * 1024;
 constexpr int SHORT_BYTES = 512 * 1024;
 constexpr int SMEM_FIXED = 1024 + BAR_BYTES;
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
           if (it < p.tiles) rows(it);
         }
       };
-      const int ahead = min(4, ks1 - ks0);  // the weights', before the wait for the tokens'
+      const int ahead = min(SF_AHEAD, ks1 - ks0);  // the weights', before the wait for the tokens'
       for (int j = 0; j < ahead; ++j) weights(ks0 + j, j);
       griddep_wait();
       for (int j = 0; j < SF_AHEAD; ++j) {
@@ -750,7 +751,7 @@ Params plan(int T, int N, int K) {
       if (rows * (merged ? 2 : 1) > 128 || (s > 1 && (s * T > MAX_N || s > p.KB))) continue;
       const int stage = (GATEUP ? 2 : 1) * rows * ROW_BYTES + n * ROW_BYTES;
       const int cols = ops * n + (MX ? 2 * SF_SLOT_COLS : 16) + (p.tail ? ops * p.tail_n : 0);
-      if (s > 1 && (cols > 512 || 4 * stage > RING_ALONE - (MX ? SF_SLOTS * 2048 : 40 * 1024))) continue;
+      if (s > 1 && (cols > 512 || 4 * stage > RING_ALONE - (MX ? SF_SLOTS * 1536 : 40 * 1024))) continue;
       // a staged epilogue's accumulators fit where the ring (four stages at least) was
       if ((s > 1 || merged) && 512 * ops * (s * (T + MAX_CLUSTER - 1) + (p.tail ? T + 1 : 0)) > 4 * stage) continue;
       const float cost = (150.f + 4 * ops * (32.f + n / 8.f) + (MX ? 60.f * (ops + 1) : 0.f)) / s;
