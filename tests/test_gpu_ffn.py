@@ -174,6 +174,68 @@ def test_mxfp8_few_and_many_tokens_agree(moe):
     assert float(d) < 2.0 ** -8
 
 
+def run_mxfp8(moe, T, H, F, x, x_sf, w):
+    cfg = moe.make_ffn_config(T, H, F, dtype="mxfp8")
+    y = torch.empty((T, H), dtype=BF, device="cuda")
+    moe.moe_ffn_fwd(cfg, x, x_sf, w[0][0], w[1][0], w[2][0], w[0][1], w[1][1], w[2][1], y, None,
+                    moe.workspace(moe.moe_ffn_workspace_size(cfg)).fill_(255))
+    torch.cuda.synchronize()
+    assert moe.moe_get_device_status() == 0
+    return y
+
+
+@pytest.mark.parametrize("T", [3, 16, 17, 130])
+@pytest.mark.parametrize("H,F", [(1024, 512), (768, 640)])
+def test_mxfp8_scales_at_any_word(moe, T, H, F):
+    """Scales that start 4 bytes past a 16-byte boundary (four k-blocks are read at a time where they may be)."""
+    x, W_g, W_u, W_d = inputs(T, H, F)
+    w = [mx_of(moe, v) for v in (W_g, W_u, W_d)]
+    xq, xs = mx_of(moe, x)
+
+    def moved(s):
+        m = torch.full((s.numel() + 16,), 255, dtype=torch.uint8, device="cuda")[4:4 + s.numel()].view(s.shape)
+        return m.copy_(s)
+
+    ref = run_mxfp8(moe, T, H, F, xq, xs, w)
+    assert torch.equal(run_mxfp8(moe, T, H, F, xq, moved(xs), [(q, moved(s)) for q, s in w]), ref)
+
+
+@pytest.mark.parametrize("T", [4, 80])
+def test_mxfp8_nan_stays_in_its_row(moe, T):
+    H, F = 512, 256
+    x, W_g, W_u, W_d = inputs(T, H, F)
+    w = [mx_of(moe, v) for v in (W_g, W_u, W_d)]
+    ref = run_mxfp8(moe, T, H, F, x, None, w)
+    bad = x.clone()
+    bad[1, 7] = float("nan")
+    y = run_mxfp8(moe, T, H, F, bad, None, w)
+    keep = [t for t in range(T) if t != 1]
+    assert torch.equal(y[keep], ref[keep])
+    assert bool(torch.isnan(y[1]).all())
+
+
+@pytest.mark.parametrize("T,H,F", [(128, 512, 4096), (200, 4096, 1024)])
+def test_cut_tiles_repeat(moe, T, H, F):
+    """Tiles that are cut along K are added in a fixed order, whatever the pieces' timing."""
+    x, W_g, W_u, W_d = inputs(T, H, F)
+    w = [mx_of(moe, v) for v in (W_g, W_u, W_d)]
+    one = forward(moe, x, W_g, W_u, W_d)[1], run_mxfp8(moe, T, H, F, x, None, w)
+    for _ in range(5):
+        assert torch.equal(forward(moe, x, W_g, W_u, W_d)[1], one[0])
+        assert torch.equal(run_mxfp8(moe, T, H, F, x, None, w), one[1])
+
+
+def test_refuses_tensors_elsewhere(moe):
+    x, W_g, W_u, W_d = inputs(4, 64, 64)
+    cfg = moe.make_ffn_config(4, 64, 64)
+    ws = moe.workspace(moe.moe_ffn_workspace_size(cfg))
+    y = torch.empty_like(x)
+    with pytest.raises(ValueError):
+        moe.moe_ffn_fwd(cfg, x.cpu(), None, W_g, W_u, W_d, None, None, None, y, None, ws)
+    with pytest.raises(ValueError):
+        moe.moe_rmsnorm_fwd(x, None, W_g[0].contiguous(), 1e-6, None, y.cpu(), None, None, None)
+
+
 # ------------------------------------------------------------------ special values, graphs, streams, the chain
 
 @pytest.mark.parametrize("T", [4, 80])
