@@ -30,6 +30,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "elect.cuh"
@@ -973,7 +974,7 @@ int launch_dep(K kern, dim3 grid, int threads, size_t smem, int cluster, cudaStr
 // Pairs of CTAs that can be resident at once on the current device.
 template <int OP>
 int max_pairs() {
-  static int cached[64] = {};
+  static std::atomic<int> cached[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     (void)cudaGetLastError();
@@ -999,7 +1000,7 @@ int max_pairs() {
     }
     cached[dev] = n > 0 ? n : -1;
   }
-  return cached[dev] > 0 ? cached[dev] : 0;
+  return std::max(cached[dev].load(), 0);
 }
 
 // Form and work split of a product, chosen before its tensor maps are made (the form sets the boxes of B).

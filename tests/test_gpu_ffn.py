@@ -152,9 +152,15 @@ def test_forward_mxfp8(moe, T, H, F):
     # An element of a whose fp32 value falls on the other side of a rounding border moves by one e4m3 step, at most
     # 2^-3 of it; a block whose maximum crosses a power of two changes all of it. fp32 dot products are off by about
     # sqrt(H) 2^-24 of their terms' size, so that a share of some sqrt(H) 2^-24 / 2^-4 of the elements (below 1 in
-    # 1000 for H <= 8192) does: terms' errors of root mean square sqrt(1e-3) / 8
+    # 1000 for H <= 8192, and 1 in 10^4 for H < 10^4) does: terms' errors of root mean square sqrt(1e-3) / 8.
+    # Such an error is not small beside its term, as check_sum's are: it is 1/8 of it, or nothing. Eight deviations,
+    # sqrt(1e-3) sqrt(F) = 1.7 mean terms at F = 2944, are passed by the step of one term of 14 mean terms (of 28, if
+    # the step is the binade's finest, 1/16). Terms a d are products of three normal factors, of which one in 10^6 is
+    # that large; a row has F 1e-4 = 0.3 such steps, so of 5 10^7 outputs some tens are expected to pass, each by no
+    # more than the step of its largest term, and a second such step in one row in 10^6 of those.
     sigma = (av.pow(2) @ dv.pow(2).T).sqrt()
-    check_sum(out[0], av @ dv.T, sigma, (1e-3 ** 0.5) / 8, F)
+    step = lambda i, j: (av[i.cuda()] * dv[j.cuda()]).abs().amax(1) / 8  # noqa: E731
+    check_sum(out[0], av @ dv.T, sigma, (1e-3 ** 0.5) / 8, F, step)
 
 
 def test_mxfp8_few_and_many_tokens_agree(moe):
@@ -234,6 +240,34 @@ def test_refuses_tensors_elsewhere(moe):
         moe.moe_ffn_fwd(cfg, x.cpu(), None, W_g, W_u, W_d, None, None, None, y, None, ws)
     with pytest.raises(ValueError):
         moe.moe_rmsnorm_fwd(x, None, W_g[0].contiguous(), 1e-6, None, y.cpu(), None, None, None)
+
+
+# ------------------------------------------------------------------ every form of the dense kernel
+# One CTA or a pair, 128 or 256 columns, whole tiles or a last round cut along K (a piece per CTA, or one line), and
+# both orders of the tiles, alone and in groups of panels: on 148 SMs these sizes take each for every product.
+
+FORMS = [
+    (69, 64, 64), (278, 4904, 64), (327, 64, 9560), (4487, 64, 1568), (65, 1104, 6304),
+    (4848, 1584, 64), (1543, 5496, 64), (72, 6192, 1312), (1822, 64, 2336), (70, 5640, 5592),
+    (73, 6392, 3856), (3913, 144, 9488), (73, 1856, 8320), (5108, 72, 3080), (139, 6920, 1672),
+    (150, 6688, 5016), (135, 2384, 8576), (68, 6752, 6440), (3311, 680, 6592), (3265, 272, 5632),
+    (268, 6568, 4544), (172, 6488, 9512), (5422, 4720, 5608), (5296, 5400, 2544), (2359, 2088, 6032),
+    (2151, 2360, 5984), (5343, 6480, 4744)]
+FORMS_MX = [
+    (17, 256, 128), (260, 256, 6528), (388, 9728, 128), (17, 256, 10112), (3620, 2560, 128),
+    (18, 8960, 9984), (20, 7936, 3200), (2314, 256, 1024), (141, 6656, 1792), (139, 3328, 7040),
+    (129, 9728, 9600), (5224, 9728, 2944), (5860, 9472, 2816), (4661, 4608, 11392),
+    (4655, 5888, 10880)]
+
+
+@pytest.mark.parametrize("T,H,F", FORMS)
+def test_forms_bf16(moe, T, H, F):
+    test_backward_bf16(moe, T, H, F)
+
+
+@pytest.mark.parametrize("T,H,F", FORMS_MX)
+def test_forms_mxfp8(moe, T, H, F):
+    test_forward_mxfp8(moe, T, H, F)
 
 
 # ------------------------------------------------------------------ special values, graphs, streams, the chain
