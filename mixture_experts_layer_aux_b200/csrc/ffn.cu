@@ -272,12 +272,6 @@ static int stream_gemm(int T, int N, int K, const void* W0, const void* W1, cons
   p.sf0 = sf0;
   p.sf1 = sf1;
   p.x_sf = x_sf;
-  if (MX) {  // the widest copies that the scales' rows allow
-    const uintptr_t at = reinterpret_cast<uintptr_t>(sf0) | reinterpret_cast<uintptr_t>(sf1) |
-                         reinterpret_cast<uintptr_t>(x_sf) | (uintptr_t)(K / 32);
-    p.gran = 4 * p.s;
-    while (at % p.gran != 0) p.gran /= 2;
-  }
   p.out = out;
   p.ldo = ldo;
   p.out_sf = out_sf;
