@@ -1,5 +1,5 @@
-// dense.cuh -- dense bf16 GEMM of the gated feed-forward block on the sm_100a
-// tensor cores (tcgen05 + TMEM + TMA), any M, and N, K multiples of 8:
+// dense.cuh -- dense GEMMs of the gated feed-forward block on the sm_100a tensor
+// cores (tcgen05 + TMEM + TMA), in bf16 for any M, and N, K multiples of 8:
 //   gate/up   a   = silu(x W_g^T) * (x W_u^T)     (both projections in one tile: [gate | up] columns)
 //   down      y   = a W_d^T
 //   dgrad     dgu = SwiGLU backward of (dY W_d),  dX = dgate W_g + dup W_u
@@ -17,8 +17,9 @@
 // Template BN: 256, or 128 where that fills the SMs better. plan() chooses.
 // Roles (320 threads, one CTA per SM, persistent), as in the grouped GEMM of
 // gemm.cuh: warp 0 TMA producer, warp 1 MMA issuer (the pair's first CTA) and
-// TMEM owner (two BN-column accumulators), warps 2..9 epilogue (lane quadrant
-// w % 4, column half). Every wait is bounded (MOE_WAIT_NS).
+// TMEM owner (two BN-column accumulators; one of 256 columns with MXFP8), warps
+// 2..9 epilogue (lane quadrant w % 4, column half), with MXFP8 warp 10 loader of
+// the scales. Every wait is bounded (MOE_WAIT_NS).
 //
 // Work split. Whole tiles go round robin over the CTAs (pairs) while they fill
 // every SM. The tiles of a rest that would leave many idle for long are cut
@@ -56,7 +57,7 @@ enum Op : int {
   OP_DOWN = 1,       // A, B K-major: bf16
   OP_DGRAD_ACT = 2,  // A = dY K-major, B = W_d MN-major: dgate | dup from the saved gate/up
   OP_DGRAD_X = 3,    // A = dgate then dup (K-major), B = W_g then W_u (MN-major): bf16
-  OP_WGRAD = 4,      // A = dO^T, B = act^T (both MN-major): bf16; rows past m_split from A2 into C2
+  OP_WGRAD = 4,      // A = dO^T, B = act^T (both MN-major): bf16; the second half's rows from A2 into C2
   OP_GATEUP_MX = 5,  // the first two in MXFP8: e4m3 operands with a scale per 1x32 block, the activation as such
   OP_DOWN_MX = 6,
 };
@@ -65,7 +66,7 @@ constexpr bool is_gateup(int op) { return op == OP_GATEUP || op == OP_GATEUP_MX;
 
 struct __align__(64) Params {
   CUtensorMap tmA, tmA2, tmB0, tmB1;
-  int M, N;            // output rows and columns (per half when m_split)
+  int M, N;            // output rows (of one half) and columns
   int KB;              // k-blocks of 128 bytes
   int kb_split;        // OP_DGRAD_X: k-blocks of the first half
   int halves;          // OP_WGRAD: 2 for two stacked outputs of M rows each (A2, C2 the second), else 1

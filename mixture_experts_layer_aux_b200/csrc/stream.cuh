@@ -6,8 +6,8 @@
 // side (128 rows of an MMA), the tokens the N side, so nothing is padded to 128
 // tokens. What would be the tile's height is free instead: a CTA owns
 // r = ceil(rows / SMs) weight rows (the height of its TMA boxes, any number up
-// to 128), so that every SM streams the same number of bytes, K is never split
-// over CTAs and no partial sums are exchanged.
+// to 128), so that every SM streams the same number of bytes, and K is split over
+// CTAs only where a cluster shares a tile (plan()), through shared memory.
 //   gate/up  r columns of F: r rows of W_g and r rows of W_u; the SwiGLU (MXFP8:
 //            and the 1x32 quantisation of the activation, r a multiple of 32)
 //            is the epilogue;
@@ -24,7 +24,7 @@
 // Operand rows that no box fills read whatever lies behind it in shared memory;
 // a row (column) of the accumulator depends on its own operand row alone, and
 // those are not stored.
-// Stages go through a ring of up to 95 KB, so that two CTAs fit on an SM: the
+// Where there is little to stream, the ring leaves room for a second CTA: the
 // down kernel starts while the gate/up kernel ends (programmatic dependent
 // launch), and its first weights, which depend on nothing, are on their way
 // before it waits for the activation.
@@ -742,8 +742,9 @@ Params plan(int T, int N, int K) {
   p.tail_n = (T + 15) / 16 * 16;
   p.z = p.tail || K % kstep == 0;
   p.KB = p.z ? K / kstep : (K + kstep - 1) / kstep;
-  // K blocks per stage, and gate and up in one operand or in two: what costs the MMA issuer least per block (a wait
-  // and a commit 150 ns, an MMA 32 + N / 8, a copy of scales 60), as far as operand rows, TMEM and the ring allow
+  // K blocks per stage, and gate and up in one operand or in two: what costs the MMA issuer least per block (measured
+  // with one thread in its loop, in ns: a wait and a commit 150, an MMA 32 + N / 8, a copy of scales 60), as far as
+  // operand rows, TMEM and the ring allow
   float best = 1e30f;
   for (int merged = 0; merged <= (GATEUP && one ? 1 : 0); ++merged)
     for (int s = 1; s <= (one && p.z ? (MX ? 4 : MAX_PARTS - 1) : 1); s += MX ? s : 1) {
