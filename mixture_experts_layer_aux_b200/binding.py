@@ -138,26 +138,27 @@ def _p(t):
     return t.data_ptr()
 
 
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _st(stream):
     if stream is None:
         # the current stream's handle, without building a torch.cuda.Stream (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _current_stream(_current_device())
     return stream.cuda_stream
+
+
+def _elsewhere(t, dev):
+    if t.get_device() != dev:
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    raise AssertionError("contiguous tensors only")
 
 
 def _ps(*tensors):
     """Pointers of device tensors (or None) that must all live on the current device, where the call launches."""
-    dev = torch._C._cuda_getDevice()
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
-        assert t.is_contiguous()
-        out.append(t.data_ptr())
-    return out
+    dev = _current_device()
+    return [None if t is None else
+            t.data_ptr() if t.get_device() == dev and t.is_contiguous() else _elsewhere(t, dev) for t in tensors]
 
 
 def _nbytes(ws):
@@ -367,9 +368,9 @@ def moe_layer_bwd_mxfp8(cfg, dY, d_aux, x, W_r, W_dT, W_dT_sf, W_guT, W_guT_sf, 
 
 def moe_rmsnorm_fwd(x, residual, weight, eps, h, y, y_q, y_sf, rstd, stream=None):
     """x, residual [..., H] bf16 (residual or None); outputs h, y, y_q + y_sf, rstd may each be None."""
-    H = x.shape[-1]
-    return _check("moe_rmsnorm_fwd", load().moe_rmsnorm_fwd(
-        x.numel() // H, H, *_ps(x, residual, weight), eps, *_ps(h, y, y_q, y_sf, rstd), _st(stream)))
+    H = x.size(-1)
+    x_, r_, w_, *out = _ps(x, residual, weight, h, y, y_q, y_sf, rstd)
+    return _check("moe_rmsnorm_fwd", load().moe_rmsnorm_fwd(x.numel() // H, H, x_, r_, w_, eps, *out, _st(stream)))
 
 
 def moe_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
@@ -378,7 +379,7 @@ def moe_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
 
 def moe_rmsnorm_bwd(dY, h, weight, rstd, dh, dX, dweight, ws, stream=None):
     """dh (the upstream of h), dX, dweight may be None; ws only with dweight."""
-    H = h.shape[-1]
+    H = h.size(-1)
     return _check("moe_rmsnorm_bwd", load().moe_rmsnorm_bwd(
         h.numel() // H, H, *_ps(dY, h, weight, rstd, dh, dX, dweight, ws), _nbytes(ws), _st(stream)))
 
