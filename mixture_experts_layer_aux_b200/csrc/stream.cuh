@@ -439,15 +439,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
       // past the end of K (of a last stage) or a row past the weights is zero-filled.
       constexpr int WJ = 4, XJ = 4 * MAX_T_MX / 32;
       const uint8_t *w0[WJ], *xs[XJ];
-      int wc[WJ], wd[WJ], xc[XJ];
+      int wc[WJ], wb[WJ], wd[WJ], xc[XJ];
       const long long w1 = GATEUP ? p.sf1 - p.sf0 : 0;
       const auto rows = [&](int t) {
 #pragma unroll
         for (int j = 0; j < WJ; ++j) {
           const int e = lane + 32 * j, c = (e >= p.r) + (e >= 2 * p.r) + (e >= 3 * p.r), i = e - c * p.r;  // s <= 4
           const long long n = (long long)t * p.r + i;
-          w0[j] = p.sf0 + n * kw + 4 * c;
-          wc[j] = e < p.s * p.r && n < p.N ? c : 1 << 20;
+          const bool in = e < p.s * p.r && n < p.N;
+          w0[j] = in ? p.sf0 + n * kw + 4 * c : p.sf0;
+          wc[j] = in ? c : 1 << 20;
+          wb[j] = in ? 4 : 0;
           wd[j] = p.merged ? chunk_offset(e + p.w_rows) : p.sf_w1 + chunk_offset(e);
         }
       };
@@ -458,8 +460,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
         xs[j] = p.x_sf + (long long)(e - c * p.T) * kw + 4 * c;
         xc[j] = c;
       }
+      // (the loader's instructions set the pace of short stages: whole stages go without the checks of the last)
+      const int wn = p.s * p.r, xn = p.s * p.T;
       const auto weights = [&](int ks, int st) {
         uint8_t* sf = sf_ring + st * p.sf_bytes;
+        if ((ks + 1) * p.s <= p.KB) {
+          const long long at = 4 * ks * p.s;
+#pragma unroll
+          for (int j = 0; j < WJ; ++j) {
+            if (32 * j >= wn) break;
+            if (lane + 32 * j < wn) {
+              cp_async4(sf + 16 * lane + 4 * j, w0[j] + at, wb[j]);
+              if (GATEUP) cp_async4(sf + wd[j], w0[j] + at + w1, wb[j]);
+            }
+          }
+          return;
+        }
 #pragma unroll
         for (int j = 0; j < WJ; ++j) {
           if (lane + 32 * j >= p.s * p.r) continue;
@@ -471,6 +487,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
       };
       const auto tokens = [&](int ks, int st) {
         uint8_t* sf = sf_ring + st * p.sf_bytes + p.sf_x;
+        if ((ks + 1) * p.s <= p.KB) {
+          const long long at = 4 * ks * p.s;
+#pragma unroll
+          for (int j = 0; j < XJ; ++j) {
+            if (32 * j >= xn) break;
+            if (lane + 32 * j < xn) cp_async4(sf + 16 * lane + 4 * j, xs[j] + at, 4);
+          }
+          return;
+        }
 #pragma unroll
         for (int j = 0; j < XJ; ++j) {
           if (lane + 32 * j >= p.s * p.T) continue;
