@@ -579,24 +579,30 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
       uint32_t cur[C::SF_BLOCKS][4][SF_KB], nxt[C::SF_BLOCKS][4][SF_KB];
       Seg s = walk.next(p);
       int base = s.kb0 / SF_KB * SF_KB;  // the batch in nxt: k-blocks base .. base + SF_KB - 1 of s
-      const auto fetch = [&] {
+      const uint8_t* src[C::SF_BLOCKS][4];  // this lane's rows
+      uint32_t in = 0;                       // which of them exist
+      const auto rows = [&] {
         const Origin o = origin<OP, CG, BN>(p, s.tile, rank);
+        in = 0;
 #pragma unroll
         for (int b = 0; b < C::SF_BLOCKS; ++b)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int r = 128 * b + 32 * i + lane, n = r - BM;
-            const uint8_t* src = nullptr;
-            if (b == 0) {
-              if (r < o.rows) src = p.sfa + (o.m0 + r) * p.ld_sf;
-            } else if (C::GATEUP) {
-              const int c = n % (BN / 2);
-              if (c < o.cols) src = (n < BN / 2 ? p.sfb0 : p.sfb1) + (long long)(o.n0 + c) * p.ld_sf;
-            } else if (n < o.cols) {
-              src = p.sfb0 + (long long)(o.n0 + n) * p.ld_sf;
-            }
+            const int r = 128 * b + 32 * i + lane, n = r - BM, c = C::GATEUP ? n % (BN / 2) : n;
+            const bool ok = b == 0 ? r < o.rows : c < o.cols;
+            if (b == 0) src[b][i] = p.sfa + (o.m0 + r) * p.ld_sf;
+            else src[b][i] = (C::GATEUP && n >= BN / 2 ? p.sfb1 : p.sfb0) + (long long)(o.n0 + c) * p.ld_sf;
+            in |= (ok ? 1u : 0u) << (4 * b + i);
+          }
+      };
+      const auto fetch = [&] {
+#pragma unroll
+        for (int b = 0; b < C::SF_BLOCKS; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool ok = (in >> (4 * b + i)) & 1u;
             if (p.sf16) {
-              const uint4 w = src ? *reinterpret_cast<const uint4*>(src + 4 * base) : make_uint4(0, 0, 0, 0);
+              const uint4 w = ok ? *reinterpret_cast<const uint4*>(src[b][i] + 4 * base) : make_uint4(0, 0, 0, 0);
               nxt[b][i][0] = w.x;
               nxt[b][i][1] = w.y;
               nxt[b][i][2] = w.z;
@@ -604,13 +610,16 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
             } else {
 #pragma unroll
               for (int k = 0; k < SF_KB; ++k)
-                nxt[b][i][k] = src && base + k < p.KB ? reinterpret_cast<const uint32_t*>(src)[base + k] : 0;
+                nxt[b][i][k] = ok && base + k < p.KB ? reinterpret_cast<const uint32_t*>(src[b][i])[base + k] : 0;
             }
           }
       };
       int stage = 0;
       uint32_t phase = 0;
-      if (s.tile >= 0) fetch();
+      if (s.tile >= 0) {
+        rows();
+        fetch();
+      }
       while (s.tile >= 0 && !aborted) {
         const int k0 = max(s.kb0 - base, 0), k1 = min(s.kb0 + s.nkb - base, SF_KB);  // the batch's k-blocks
 #pragma unroll
@@ -623,6 +632,7 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
         if (base >= s.kb0 + s.nkb) {
           s = walk.next(p);
           base = s.kb0 / SF_KB * SF_KB;
+          if (s.tile >= 0) rows();
         }
         if (s.tile >= 0) fetch();
 #pragma unroll
