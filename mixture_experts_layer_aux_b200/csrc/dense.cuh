@@ -165,8 +165,13 @@ MOE_DEV Origin origin(const Params& p, int tile, int rank) {
   Origin o;
   // the tiles of p.group rows (or columns) by turns, along all columns (rows)
   const int fast = p.n_fast ? p.tiles_n : p.tiles_m, slow = p.n_fast ? p.tiles_m : p.tiles_n;
-  const int g = tile / (p.group * slow), i = tile - g * p.group * slow, w = min(p.group, fast - g * p.group);
-  const int ft = g * p.group + i % w, st = i / w;
+  int f0 = 0, i = tile, w = fast;
+  if (p.group < fast) {
+    f0 = tile / (p.group * slow) * p.group;
+    i -= f0 * slow;
+    w = min(p.group, fast - f0);
+  }
+  const int st = i / w, ft = f0 + i - st * w;
   const int mt = p.n_fast ? st : ft, nt = p.n_fast ? ft : st;
   o.second = OP == OP_WGRAD && mt >= p.tm_split;
   o.m0 = (mt - (o.second ? p.tm_split : 0)) * BM * CG + rank * BM;
