@@ -578,8 +578,9 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
     // needs all). They join their stage: the loader waits for the stage as the producer does, and arrives on its
     // barrier. A lane reads the words of SF_KB k-blocks of rows l, l + 32, l + 64, l + 96 of a block of 128, one batch
     // ahead, and writes, per k-block, these rows' words as the 16 bytes l of its chunk; one proxy fence for two
-    // k-blocks (8192 tokens, H = 7168, F = 2048: 290 us; with a second loader and a fence for each, 298; with barriers
-    // of their own for four k-blocks at a time, 360).
+    // k-blocks, and no more instructions than that takes: they set the pace (8192 tokens, H = 7168, F = 2048: 270 us;
+    // with the rows' addresses computed for each batch 290, with a second loader and a fence for each k-block besides
+    // 298, with barriers of their own for four k-blocks at a time 360).
     if constexpr (C::MX) {
       uint32_t cur[C::SF_BLOCKS][4][SF_KB], nxt[C::SF_BLOCKS][4][SF_KB];
       Seg s = walk.next(p);
@@ -1035,16 +1036,17 @@ constexpr int GROUP_ROWS = 2048;
 
 // The form of least estimated time: rounds of tiles times k-blocks times a k-block's time, measured in us (down
 // projection, T = H = F = 4096, all in one launch: 97.9 us with one CTA and 256 columns, 109.0 with 128, pairs 82.1 and
-// 91.2, MXFP8 57.9, 71.3, 57.4 and 71.7; 24 k-blocks of T = 1001, H = 2048: 14.4, 11.6, 14.4 and 12.3). Cutting the
+// 91.2, MXFP8 57.4, 63.8, 49.8 and 57.9; 24 k-blocks of T = 1001, H = 2048: 14.4, 11.6, 14.4 and 12.3). Cutting the
 // tiles of the last round along K saves the idle part of that round and costs partial sums out and in again and one
-// more kernel: 5 us and about 1.2 per piece of a tile where every CTA has one piece (T = 128, H = 4096, F = 14336, one
-// CTA and 128 columns: 55.8 us whole, 38.9 in 2 pieces, 34.8 in 3, 32.6 in 4; 256 columns 87.9, 54.1, 45.3, 39.0, 34.9
-// in 8). A rest of more than half a round cannot be cut so; there the line of its k-blocks is cut into equal pieces,
-// of which most CTAs have two (13 us).
+// more kernel: where every CTA has one piece 4 us for 2 pieces a tile to 8 for 8, and half as much again to twice that
+// where its rows are all there (MXFP8 gate/up, H = 7168, F = 2048, 32 tokens, one CTA and 128 columns: 18.5 us whole,
+// 16.0 in 2 pieces, 14.4 in 4; 128 tokens: 20.5, 18.5 and 19.1; down, H = 4096, F = 14336, 128 tokens: 55.8, 38.9 and
+// 32.6). A rest of more than half a round cannot be cut so; there the line of its k-blocks is cut into equal pieces, of
+// which most CTAs have two (13 us). A pair takes 1 us more to set up and to leave.
 template <int OP>
 Plan plan(Params& p) {
   static constexpr float KB_US[2][2][2] = {{{0.22f, 0.355f}, {0.185f, 0.29f}},   // bf16: [pairs][256 columns]
-                                           {{0.285f, 0.395f}, {0.29f, 0.38f}}};  // MXFP8
+                                           {{0.25f, 0.38f}, {0.22f, 0.335f}}};    // MXFP8
   int sms = moe_host::num_sms();
   if (sms > MAX_CTAS) sms = MAX_CTAS;
   const int pairs = std::min(max_pairs<OP>(), sms / 2);
@@ -1072,14 +1074,16 @@ Plan plan(Params& p) {
         p.sk_per = sk_per;
         p.sk_kb = sk_kb;
       };
-      take((rounds + (rest ? 1 : 0)) * p.KB * kb, 0, 0, p.KB);
+      const float filled = (float)p.M / (per * BM * cg), fix = cg == 2 ? 1.f : 0.f;
+      take((rounds + (rest ? 1 : 0)) * p.KB * kb + fix, 0, 0, p.KB);
       for (int n = 2; rest > 0 && n <= MAX_PIECES && rest * n <= workers && n <= p.KB; ++n) {
         const int len = (p.KB + n - 1) / n, used = (p.KB + len - 1) / len;  // pieces of a tile, none empty
-        take((rounds * p.KB + len) * kb + 5.f + 1.2f * used, rest, len, len * used);
+        const float join = 3.f + 0.6f * used + filled * (2.f + 0.8f * used);
+        take((rounds * p.KB + len) * kb + fix + join, rest, len, len * used);
       }
       if (2 * rest > workers) {
         const int len = (rest * p.KB + workers - 1) / workers;
-        take((rounds * p.KB + len) * kb + 13.f, rest, len, p.KB);
+        take((rounds * p.KB + len) * kb + fix + 13.f, rest, len, p.KB);
       }
     }
   }

@@ -257,7 +257,8 @@ FORMS_MX = [
     (17, 256, 128), (260, 256, 6528), (388, 9728, 128), (17, 256, 10112), (3620, 2560, 128),
     (18, 8960, 9984), (20, 7936, 3200), (2314, 256, 1024), (141, 6656, 1792), (139, 3328, 7040),
     (129, 9728, 9600), (5224, 9728, 2944), (5860, 9472, 2816), (4661, 4608, 11392),
-    (4655, 5888, 10880)]
+    (4655, 5888, 10880),
+    (17, 9984, 1792), (17, 256, 4992), (21, 9984, 3584), (21, 6400, 11392), (132, 3584, 11264)]
 
 
 @pytest.mark.parametrize("T,H,F", FORMS)
