@@ -16,9 +16,10 @@ namespace ffn {
 
 using dense::Params;
 
-// Tokens up to which the streaming kernels are taken. MXFP8: their loader fetches the scales by the word, the dense
-// kernel's by four (H = 7168, F = 2048: 16 tokens 26.9 us streaming and 30.6 dense, 32 tokens 31.0 and 28.0; H = 4096,
-// F = 14336: 8 tokens 57.7 and 57.2, 32 tokens 62.0 and 49.4).
+// Tokens up to which the streaming kernels are taken: 56 (bf16, H = 2048, F = 5504: 48 tokens 28.7 us streaming and
+// 30.9 dense, 64 tokens 32.6 and 30.6; 4096 x 14336: 72.9 and 75.3, 74.9 and 76.1), 16 for MXFP8, whose loader of scales
+// sets the pace there (H = 7168, F = 2048: 16 tokens 23.4 us and, at an earlier stage of both, 26.9 and 30.6; 32 tokens
+// then 31.0 and 28.0, now dense 27.2).
 static bool streams(const moe_ffn_config* c) {
   return c->T <= (c->dtype == MOE_DT_MXFP8 ? stream::MAX_T_MX : stream::MAX_T);
 }

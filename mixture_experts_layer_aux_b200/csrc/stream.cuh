@@ -54,7 +54,7 @@ bool encode_tmap_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, ui
 
 namespace stream {
 
-constexpr int MAX_T = 64, MAX_T_MX = 16;
+constexpr int MAX_T = 56, MAX_T_MX = 16;
 constexpr int MAX_STAGES = 16;
 constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
 constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
