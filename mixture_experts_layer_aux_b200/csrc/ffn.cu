@@ -57,9 +57,9 @@ struct Mat {
 };
 
 // Rows that do not start on 128 bytes cost more to load (every 128-byte row of a TMA box is on two lines), so the
-// buffers of this file are padded to 64 elements. The caller's ragged operands are read as they are: copied to padded
-// buffers first, once per call, they made a training step of T = 4001, H = 4104, F = 8200 2 % faster and the other way
-// round 8 % at T = 2200, H = 2056, F = 5464 and 17 % at T = 600, H = 4104, F = 8200.
+// buffers of this file are padded to 64 elements. The caller's ragged operands are read as they are: copies with padded
+// rows, made once per call, made a training step of T = 4001, H = 4104, F = 8200 2 % faster, but one of T = 2200,
+// H = 2056, F = 5464 7 % slower and one of T = 600, H = 4104, F = 8200 17 %.
 
 struct FwdWs {
   __nv_bfloat16* a;  // [T, Fp]
