@@ -249,10 +249,11 @@ MOE_DEV void commit(uint64_t* bar) {
                    : "memory");
   }
 }
-// Arrives on the first CTA's barrier. What the arrival stands for is done by then: accumulators are in registers
-// (tcgen05.wait::ld), and scales in this SM's shared memory, for its tensor core to read (proxy fence). A release at the
-// cluster's scope would also wait for every access to global memory in flight: 1 us per tile, and 0.9 us per k-block
-// of MXFP8, whose MMAs take 0.35.
+// Arrives on the first CTA's barrier, relaxed. For accumulators that is all: they are in registers (tcgen05.wait::ld and
+// the tcgen05 fences order them). Scales are ordinary stores to this SM's shared memory which the first CTA's
+// tcgen05.cp reads, and a proxy fence orders no threads: release_smem_cluster() goes before their arrival, and the
+// issuer waits with the matching acquire. A release of all memory at the cluster's scope would also wait for every
+// access to global memory in flight: 1 us per tile, and 0.9 us per k-block of MXFP8, whose MMAs take 0.35.
 template <int CG>
 MOE_DEV void arrive_first(uint64_t* bar) {
   if constexpr (CG == 1)
@@ -524,7 +525,12 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         for (int kb = 0; kb < s.nkb; ++kb) {
-          if (!mbar_wait_warp(&full[stage], phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA)) {
+          bool ready;
+          if constexpr (C::MX && CG == 2)  // the other CTA's scales too
+            ready = mbar_wait_warp_cluster(&full[stage], phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA);
+          else
+            ready = mbar_wait_warp(&full[stage], phase, abort_flag, p.status, DEV_WAIT_TIMEOUT_MMA);
+          if (!ready) {
             aborted = true;
             break;
           }
@@ -665,6 +671,7 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
+            if (CG == 2) release_smem_cluster();
             if (st[0] >= 0) arrive_first<CG>(&full[st[0]]);
             if (st[1] >= 0) arrive_first<CG>(&full[st[1]]);
           }

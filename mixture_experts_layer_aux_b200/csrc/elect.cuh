@@ -22,3 +22,32 @@ MOE_DEV bool elect_one() {
 MOE_DEV bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int code) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, code));
 }
+// The same for a barrier on which another CTA of the cluster arrives with relaxed.cluster after release_smem_cluster():
+// that CTA's ordinary stores to its shared memory are visible after it. The phase is observed at the cluster's scope, and
+// the acquire is restricted to shared memory, so that it waits for no access to global memory.
+MOE_DEV bool mbar_wait_warp_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int code) {
+  uint32_t ok = 0;
+  uint64_t t0 = 0;
+  while (true) {
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) break;
+    if (*abort) break;
+    if (t0 == 0) t0 = globaltimer_ns();
+    if (globaltimer_ns() - t0 > MOE_WAIT_NS) {
+      *abort = 1;
+      record_status(status, code);
+      break;
+    }
+  }
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+// Before a relaxed.cluster arrival: this thread's stores to its CTA's shared memory (and those it has observed) come
+// before the arrival for whoever waits for it with mbar_wait_warp_cluster.
+MOE_DEV void release_smem_cluster() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
