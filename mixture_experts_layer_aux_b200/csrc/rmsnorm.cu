@@ -9,7 +9,8 @@
 // Both are bound by memory: a row is read once, held in registers (V vectors
 // of 8 bf16 per thread), reduced with one block barrier and written once.
 // CTAs are persistent over rows, so the weight stays in registers and the next
-// row's loads are in flight while the current row is reduced and written.
+// row's loads are in flight while the current row is reduced and written. Rows
+// are counted unsigned: T goes up to 2^31 - 1, and a CTA's next row passes it.
 #include "common.cuh"
 #include "gemm_mx.cuh"
 #include "layout.h"
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(const FwdParams p) {
   const int nwarp = blockDim.x >> 5;
   uint4 w[V], cx[V], cr[V];
   bool ok[V];
-  auto load = [&](int row, uint4 (&a)[V], uint4 (&b)[V]) {
+  auto load = [&](uint32_t row, uint4 (&a)[V], uint4 (&b)[V]) {
     const long long base = (long long)row * p.H;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(const FwdParams p) {
   }
   load(blockIdx.x, cx, cr);
   int flip = 0;
-  for (int row = blockIdx.x; row < p.T; row += gridDim.x) {
+  for (uint32_t row = blockIdx.x; row < (uint32_t)p.T; row += gridDim.x) {
     float v[V][8];
     float ss = 0.f;
 #pragma unroll
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(MAX_THREADS) fwd_kernel(const FwdParams p) {
         ss += v[i][j] * v[i][j];
       }
     // the next row's loads go out before this row's reduction
-    if (row + (int)gridDim.x < p.T) load(row + gridDim.x, cx, cr);
+    if (row + gridDim.x < (uint32_t)p.T) load(row + gridDim.x, cx, cr);
     const float sum = block_sum(ss, red[flip], nwarp);
     flip ^= 1;
     const float rstd = __frsqrt_rn(sum / (float)p.H + p.eps);
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(MAX_THREADS) bwd_kernel(const BwdParams p) {
   float nr;
   bool ok[V];
   float dw[V][8];
-  auto load = [&](int row) {
+  auto load = [&](uint32_t row) {
     const long long base = (long long)row * p.H;
     nr = p.rstd[row];
 #pragma unroll
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(MAX_THREADS) bwd_kernel(const BwdParams p) {
   }
   load(blockIdx.x);
   int flip = 0;
-  for (int row = blockIdx.x; row < p.T; row += gridDim.x) {
+  for (uint32_t row = blockIdx.x; row < (uint32_t)p.T; row += gridDim.x) {
     uint4 cy[V], ch[V], cd[V];
     const float r = nr;
     float dot = 0.f;
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(MAX_THREADS) bwd_kernel(const BwdParams p) {
       ch[i] = nh[i];
       if (DH) cd[i] = nd[i];
     }
-    if (row + (int)gridDim.x < p.T) load(row + gridDim.x);
+    if (row + gridDim.x < (uint32_t)p.T) load(row + gridDim.x);
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
