@@ -161,6 +161,13 @@ def _ps(*tensors):
             t.data_ptr() if t.get_device() == dev and t.is_contiguous() else _elsewhere(t, dev) for t in tensors]
 
 
+def _i32(name, v):
+    """v as the library's int32 argument; ctypes would cut it to 32 bits without a word."""
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} = {v} does not fit 32 bits")
+    return v
+
+
 def _nbytes(ws):
     return ws.numel() * ws.element_size() if ws is not None else 0
 
@@ -369,24 +376,26 @@ def moe_layer_bwd_mxfp8(cfg, dY, d_aux, x, W_r, W_dT, W_dT_sf, W_guT, W_guT_sf, 
 def moe_rmsnorm_fwd(x, residual, weight, eps, h, y, y_q, y_sf, rstd, stream=None):
     """x, residual [..., H] bf16 (residual or None); outputs h, y, y_q + y_sf, rstd may each be None."""
     H = x.size(-1)
+    T = _i32("T", x.numel() // H)
     x_, r_, w_, *out = _ps(x, residual, weight, h, y, y_q, y_sf, rstd)
-    return _check("moe_rmsnorm_fwd", load().moe_rmsnorm_fwd(x.numel() // H, H, x_, r_, w_, eps, *out, _st(stream)))
+    return _check("moe_rmsnorm_fwd", load().moe_rmsnorm_fwd(T, _i32("H", H), x_, r_, w_, eps, *out, _st(stream)))
 
 
 def moe_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
-    return load().moe_rmsnorm_bwd_workspace_size(T, H)
+    return load().moe_rmsnorm_bwd_workspace_size(_i32("T", T), _i32("H", H))
 
 
 def moe_rmsnorm_bwd(dY, h, weight, rstd, dh, dX, dweight, ws, stream=None):
     """dh (the upstream of h), dX, dweight may be None; ws only with dweight."""
     H = h.size(-1)
+    T = _i32("T", h.numel() // H)
     return _check("moe_rmsnorm_bwd", load().moe_rmsnorm_bwd(
-        h.numel() // H, H, *_ps(dY, h, weight, rstd, dh, dX, dweight, ws), _nbytes(ws), _st(stream)))
+        T, _i32("H", H), *_ps(dY, h, weight, rstd, dh, dX, dweight, ws), _nbytes(ws), _st(stream)))
 
 
 def make_ffn_config(T, H, F, dtype="bf16", save_for_bwd=0) -> moe_ffn_config:
-    return moe_ffn_config(T=T, H=H, F=F, dtype=_DTYPES[dtype] if isinstance(dtype, str) else dtype,
-                          save_for_bwd=save_for_bwd)
+    return moe_ffn_config(T=_i32("T", T), H=_i32("H", H), F=_i32("F", F),
+                          dtype=_DTYPES[dtype] if isinstance(dtype, str) else dtype, save_for_bwd=save_for_bwd)
 
 
 def moe_ffn_workspace_size(cfg) -> int:

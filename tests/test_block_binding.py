@@ -1,0 +1,32 @@
+"""The Python binding of the norm and the feed-forward block: what it refuses before the library sees it, and what it
+asks of torch (no GPU needed)."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def B():
+    from mixture_experts_layer_aux_b200 import binding
+    binding.load()
+    return binding
+
+
+def test_sizes_past_32_bits_are_refused(B):
+    """2^32 + 4 rows would be four rows to the library."""
+    T = 2 ** 32 + 4
+    with pytest.raises(ValueError, match="32 bits"):
+        B.moe_rmsnorm_bwd_workspace_size(T, 8)
+    with pytest.raises(ValueError, match="32 bits"):
+        B.moe_rmsnorm_bwd_workspace_size(4, 2 ** 32 + 8)
+    for n in ("T", "H", "F"):
+        with pytest.raises(ValueError, match="32 bits"):
+            B.make_ffn_config(**{**dict(T=4, H=8, F=8), n: 2 ** 32 + 8})
+    # a tensor of that many rows, of one row's memory, as the norm's x and h
+    x = torch.zeros(8, dtype=torch.bfloat16).expand(T, 8)
+    with pytest.raises(ValueError, match="32 bits"):
+        B.moe_rmsnorm_fwd(x, None, x[0], 1e-5, None, x, None, None, None)
+    with pytest.raises(ValueError, match="32 bits"):
+        B.moe_rmsnorm_bwd(x, x, x[0], None, None, x, None, None)
+    # the largest that fit pass the binding (the library then refuses by its own rules, or not)
+    assert B.moe_rmsnorm_bwd_workspace_size(2 ** 31 - 1, 8) == 296 * 8 * 4 + (-(296 * 8 * 4)) % 256
+    assert B.make_ffn_config(T=2 ** 31 - 1, H=8, F=8).T == 2 ** 31 - 1
