@@ -138,12 +138,15 @@ def _p(t):
     return t.data_ptr()
 
 
-_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# The current device and its stream's handle, without building a torch.cuda.Stream (3 us a call); by the public functions
+# where torch has no such names (a build without CUDA, which can still load the library and make its refusals).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _st(stream):
     if stream is None:
-        # the current stream's handle, without building a torch.cuda.Stream (3 us a call)
         return _current_stream(_current_device())
     return stream.cuda_stream
 

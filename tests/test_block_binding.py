@@ -1,7 +1,13 @@
 """The Python binding of the norm and the feed-forward block: what it refuses before the library sees it, and what it
 asks of torch (no GPU needed)."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -30,3 +36,20 @@ def test_sizes_past_32_bits_are_refused(B):
     # the largest that fit pass the binding (the library then refuses by its own rules, or not)
     assert B.moe_rmsnorm_bwd_workspace_size(2 ** 31 - 1, 8) == 296 * 8 * 4 + (-(296 * 8 * 4)) % 256
     assert B.make_ffn_config(T=2 ** 31 - 1, H=8, F=8).T == 2 ** 31 - 1
+
+
+def python(code):
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_a_torch_without_cuda_is_enough_for_the_refusals():
+    """A build of torch without CUDA has none of these names."""
+    python("""
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    delattr(torch._C, name)
+from mixture_experts_layer_aux_b200 import binding as b
+assert b.load().moe_rmsnorm_fwd(0, 8, None, None, None, 1e-5, None, None, None, None, None, None) == 1
+assert b.moe_ffn_workspace_size(b.make_ffn_config(1, 64, 64)) > 0
+""")
