@@ -12,16 +12,23 @@ import importlib
 __all__ = ["load"]
 
 _SUBMODULES = ("binding", "build", "synthetic")
+_names = None  # the binding's namespace, once it is imported
 
 
 def __getattr__(name):
-    if name.startswith("__") or name in _SUBMODULES:
-        if name in _SUBMODULES:
-            return importlib.import_module(f"{__name__}.{name}")
+    global _names
+    if name.startswith("__"):
         raise AttributeError(name)
-    value = getattr(importlib.import_module(f"{__name__}.binding"), name)
-    globals()[name] = value  # found directly from now on
-    return value
+    try:
+        # looked up each time (0.3 us): the binding rebinds names of its own, and a caller may
+        return _names[name]
+    except (TypeError, KeyError):
+        pass
+    if name in _SUBMODULES:
+        return importlib.import_module(f"{__name__}.{name}")
+    binding = importlib.import_module(f"{__name__}.binding")
+    _names = vars(binding)
+    return getattr(binding, name)
 
 
 def load():

@@ -53,3 +53,17 @@ from mixture_experts_layer_aux_b200 import binding as b
 assert b.load().moe_rmsnorm_fwd(0, 8, None, None, None, 1e-5, None, None, None, None, None, None) == 1
 assert b.moe_ffn_workspace_size(b.make_ffn_config(1, 64, 64)) > 0
 """)
+
+
+def test_package_names_follow_the_binding():
+    """A name of the package is the binding's at that time: the library once it is loaded, and what a caller put there."""
+    python("""
+import mixture_experts_layer_aux_b200 as moe
+assert moe._lib is None
+moe.load()
+assert moe._lib is not None
+from mixture_experts_layer_aux_b200 import binding
+assert moe.moe_ffn_saved_size is binding.moe_ffn_saved_size
+binding.moe_ffn_saved_size = len
+assert moe.moe_ffn_saved_size is len
+""")
