@@ -83,8 +83,9 @@ constexpr int SMEM_FIXED = 1024 + BAR_BYTES;
 struct __align__(64) Params {
   CUtensorMap tmW0, tmW1, tmX;
   CUtensorMap tmW0t, tmW1t, tmXt;   // the part of K past its last whole block (tail != 0): 2-D maps
-  CUtensorMap tmNext;               // gate/up: the down kernel's W0, its rows per tile, blocks per stage, tiles, and
-  int next_r, next_s, next_tiles;   // the stages to bring into L2 (from, to)
+  CUtensorMap tmNext;               // gate/up: the down kernel's W0, its rows per tile, blocks per stage, tiles, CTAs
+  int next_r, next_s, next_tiles;   // per tile and stages, and which stages of a CTA's part of K to bring into L2
+  int next_cs, next_KS;             // (from, to)
   int next_from, next_to;
   const uint8_t *sf0, *sf1, *x_sf;  // MXFP8 scales, [rows, K/32]
   void* out;                        // gate/up: bf16 or e4m3 codes; down: bf16; rows of ldo elements
@@ -107,7 +108,7 @@ struct __align__(64) Params {
   int stages, stage_bytes;
   int ring_bytes;                   // the stages, and what the last one's operands read past it
   int sf_w1, sf_x, sf_bytes;        // MXFP8: offsets of W1's and x's chunks in a slot of scales, and its size
-  int cs;                           // CTAs per tile (a cluster, each with a part of K), MXFP8 gate/up
+  int cs;                           // CTAs per tile (a cluster, each with a part of K; MXFP8 gate/up, down)
   int acc_cols, acc_bufs, tmem_cols;  // TMEM: columns of one accumulator set, sets, allocation
   int early;                        // launched over the tail of the kernel that makes x
   int merged;                       // gate/up: both weights in one operand
@@ -163,6 +164,17 @@ MOE_DEV void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// First stage of a tile's CTA `rank` of cs (1, 2 or 4), each of which takes a part of the KS stages.
+__host__ __device__ inline int part_of_k(int rank, int KS, int cs) { return rank * KS >> (cs >> 1); }
+
+// The stages of the down kernel's CTA j (tile j / cs, rank j % cs; cs is 1 or 2) to bring into L2: [from, to).
+__host__ __device__ inline void next_stages(const Params& p, int j, int& from, int& to) {
+  const int rank = j & (p.next_cs - 1), k0 = part_of_k(rank, p.next_KS, p.next_cs);
+  const int k1 = part_of_k(rank + 1, p.next_KS, p.next_cs);
+  from = k0 + p.next_from;
+  to = k0 + p.next_to < k1 ? k0 + p.next_to : k1;
+}
+
 // 4-byte asynchronous copy global -> shared; bytes 0: the destination is zeroed, nothing is read.
 MOE_DEV void cp_async4(void* smem_dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(bytes)
@@ -216,7 +228,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
   const int rank = CLUSTER ? (int)blockIdx.x % p.cs : 0;
   const int tile0 = CLUSTER ? (int)blockIdx.x / p.cs : (int)blockIdx.x;
   const int tile_step = CLUSTER ? (int)gridDim.x / p.cs : (int)gridDim.x;
-  const int ks0 = CLUSTER ? rank * p.KS / p.cs : 0, ks1 = CLUSTER ? (rank + 1) * p.KS / p.cs : p.KS;
+  const int ks0 = CLUSTER ? part_of_k(rank, p.KS, p.cs) : 0, ks1 = CLUSTER ? part_of_k(rank + 1, p.KS, p.cs) : p.KS;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -306,9 +318,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) gemm_kernel(const __grid_const
       }
     }
     if (GATEUP && elect_one())
-      for (int ks = p.next_from; ks < p.next_to && !aborted; ++ks)
-        for (int t = blockIdx.x; t < p.next_tiles; t += gridDim.x)
-          tma_prefetch_3d(&p.tmNext, 0, t * p.next_r, ks * p.next_s);
+      for (int j = blockIdx.x; j < p.next_tiles * p.next_cs && !aborted; j += gridDim.x) {
+        int ks, to;
+        next_stages(p, j, ks, to);
+        for (; ks < to; ++ks) tma_prefetch_3d(&p.tmNext, 0, (j >> (p.next_cs >> 1)) * p.next_r, ks * p.next_s);
+      }
     __syncwarp();
     if (*abort_flag) {
       // every TMA issued here must land before the CTA exits (a stage whose tokens were not asked for any more never
@@ -836,7 +850,8 @@ bool encode_maps(CUtensorMap* m, CUtensorMap* mt, const Params& p, const void* b
 }
 
 // The weights [K, N] of the down product that follows a gate/up launch: up to NEXT_BYTES of them beyond what its
-// ring takes are asked into L2 (about what memory delivers while the one kernel ends and the other begins).
+// CTAs' rings take, the same number of stages for each CTA, are asked into L2 (about what memory delivers while the one
+// kernel ends and the other begins).
 constexpr long long NEXT_BYTES = 48ll << 20;
 template <bool MX>
 bool plan_next(Params& p, const void* W_next) {
@@ -845,8 +860,10 @@ bool plan_next(Params& p, const void* W_next) {
   p.next_r = d.r;
   p.next_s = d.s;
   p.next_tiles = d.tiles;
+  p.next_cs = d.cs;
+  p.next_KS = d.KS;
   p.next_from = d.stages;
-  const long long n = d.stages + NEXT_BYTES / ((long long)d.tiles * d.s * d.r * ROW_BYTES);
+  const long long n = d.stages + NEXT_BYTES / ((long long)d.tiles * d.cs * d.s * d.r * ROW_BYTES);
   p.next_to = (int)(n < d.KS ? n : d.KS);
   return encode_map<MX>(&p.tmNext, d, W_next, d.N, d.r, d.K);
 }
