@@ -1051,12 +1051,11 @@ constexpr int GROUP_ROWS = 2048;
 // 32.6). A rest of more than half a round cannot be cut so; there the line of its k-blocks is cut into equal pieces, of
 // which most CTAs have two (13 us). A pair takes 1 us more to set up and to leave.
 template <int OP>
-Plan plan(Params& p) {
+Plan plan_for(Params& p, int sms, int pairs) {
   static constexpr float KB_US[2][2][2] = {{{0.22f, 0.355f}, {0.185f, 0.29f}},   // bf16: [pairs][256 columns]
                                            {{0.25f, 0.38f}, {0.22f, 0.335f}}};    // MXFP8
-  int sms = moe_host::num_sms();
-  if (sms > MAX_CTAS) sms = MAX_CTAS;
-  const int pairs = std::min(max_pairs<OP>(), sms / 2);
+  sms = std::min(sms, MAX_CTAS);
+  pairs = std::min(pairs, sms / 2);
   Plan c{};
   float best = 1e30f;
   for (int cg = 1; cg <= 2; ++cg) {
@@ -1099,6 +1098,11 @@ Plan plan(Params& p) {
   const int fast = p.n_fast ? p.tiles_n : p.tiles_m;
   p.group = std::min(rows_a, rows_b) * p.KB * 128 > L2_KEEP ? std::min(fast, GROUP_ROWS / (BM * c.cg)) : fast;
   return c;
+}
+
+template <int OP>
+Plan plan(Params& p) {
+  return plan_for<OP>(p, moe_host::num_sms(), max_pairs<OP>());
 }
 
 template <int OP, int CG, int BN>

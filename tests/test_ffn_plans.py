@@ -52,3 +52,20 @@ def test_down_weights_are_asked_for_evenly(host, mx):
             want = (first, last) if first < last else (-1, -1)
             assert int(rank) == k and (a0, a1) == want, line
     assert mx or split > 20
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("pairs", [74, 72])  # CTA pairs that fit the device at once
+def test_the_gpu_tests_take_every_form(host, mx, pairs):
+    """Every form of the dense GEMM that plan() gives some size of T <= 8192, H <= 10240 and F <= 16384 is taken by a
+    size of the GPU tests: for each product the CTAs per tile, the columns, and how a last round's tiles are cut; and
+    the order of the tiles."""
+    import test_gpu_ffn as a
+    import test_gpu_ffn_forms as b
+    tested = a.FORMS_MX + a.MX_SHAPES + b.FORMS_MX if mx else a.FORMS + a.SHAPES + b.FORMS
+    kind = "mx" if mx else "bf16"
+    have = {line.split()[0] for line in host("dense_plan", [kind, pairs, "list", *(v for t in tested for v in t)])}
+    found = host("dense_plan", [kind, pairs, "search", 200000, 2])
+    assert len(found) > (25 if mx else 80)
+    missing = [line for line in found if line.split()[0] not in have]
+    assert not missing, missing

@@ -244,7 +244,8 @@ def test_refuses_tensors_elsewhere(moe):
 
 # ------------------------------------------------------------------ every form of the dense kernel
 # One CTA or a pair, 128 or 256 columns, whole tiles or a last round cut along K (a piece per CTA, or one line), and
-# both orders of the tiles, alone and in groups of panels: on 148 SMs these sizes take each for every product.
+# both orders of the tiles, alone and in groups of panels: on 148 SMs these sizes, with those of test_gpu_ffn_forms.py,
+# take each that plan() gives a product (test_ffn_plans.py).
 
 FORMS = [
     (69, 64, 64), (278, 4904, 64), (327, 64, 9560), (4487, 64, 1568), (65, 1104, 6304),
