@@ -35,7 +35,8 @@ def test_the_issuer_acquires_what_the_other_cta_released():
     assert re.search(r"if constexpr \(C::MX && CG == 2\)\s*ready = mbar_wait_warp_cluster\(&full\[stage\]", issuer)
     wait = source("elect.cuh")
     wait = wait[wait.index("bool mbar_wait_warp_cluster"):]
-    assert wait.index("try_wait.parity.relaxed.cluster") < wait.index("fence.acquire.sync_restrict::shared::cluster.cluster")
+    fence = "fence.acquire.sync_restrict::shared::cluster.cluster"
+    assert wait.index("try_wait.parity.relaxed.cluster") < wait.index(fence)
 
 
 def quantised(moe, w):

@@ -69,3 +69,17 @@ def test_the_gpu_tests_take_every_form(host, mx, pairs):
     assert len(found) > (25 if mx else 80)
     missing = [line for line in found if line.split()[0] not in have]
     assert not missing, missing
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_the_gpu_tests_take_every_streaming_form(host, mx):
+    """The same for the streaming kernels, of sizes up to H, F <= 25600."""
+    import test_gpu_ffn as a
+    import test_gpu_ffn_forms as b
+    tested = a.MX_SHAPES + b.STREAM_MX if mx else a.SHAPES + b.STREAM
+    kind = "mx" if mx else "bf16"
+    have = {line.split()[0] for line in host("stream_plan", [kind, "list", *(v for t in tested for v in t)])}
+    found = host("stream_plan", [kind, "search", 200000, 3])
+    assert len(found) > (12 if mx else 25)
+    missing = [line for line in found if line.split()[0] not in have]
+    assert not missing, missing
