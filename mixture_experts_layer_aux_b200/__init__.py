@@ -12,23 +12,17 @@ import importlib
 __all__ = ["load"]
 
 _SUBMODULES = ("binding", "build", "synthetic")
-_names = None  # the binding's namespace, once it is imported
 
 
 def __getattr__(name):
-    global _names
-    if name.startswith("__"):
+    if name.startswith("__") or name in _SUBMODULES:
+        if name in _SUBMODULES:
+            return importlib.import_module(f"{__name__}.{name}")
         raise AttributeError(name)
-    try:
-        # looked up each time (0.3 us): the binding rebinds names of its own, and a caller may
-        return _names[name]
-    except (TypeError, KeyError):
-        pass
-    if name in _SUBMODULES:
-        return importlib.import_module(f"{__name__}.{name}")
-    binding = importlib.import_module(f"{__name__}.binding")
-    _names = vars(binding)
-    return getattr(binding, name)
+    value = getattr(importlib.import_module(f"{__name__}.binding"), name)
+    if not name.startswith("_"):
+        globals()[name] = value  # found directly from now on (the binding drops it where the name is bound anew)
+    return value
 
 
 def load():

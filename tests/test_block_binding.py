@@ -67,3 +67,18 @@ assert moe.moe_ffn_saved_size is binding.moe_ffn_saved_size
 binding.moe_ffn_saved_size = len
 assert moe.moe_ffn_saved_size is len
 """)
+
+
+def test_package_keeps_its_own_names():
+    """What is bound anew in the binding takes nothing from the package that is the package's own."""
+    python("""
+import mixture_experts_layer_aux_b200 as moe
+from mixture_experts_layer_aux_b200 import binding
+own = moe.load
+binding.load = binding.load
+assert moe.load is own
+f = moe.moe_ffn_saved_size
+binding.moe_ffn_saved_size = len
+binding.moe_ffn_saved_size = f
+assert moe.moe_ffn_saved_size is f and vars(moe)["moe_ffn_saved_size"] is f
+""")
