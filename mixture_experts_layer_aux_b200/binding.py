@@ -154,8 +154,8 @@ def _p(t):
     return t.data_ptr()
 
 
-# The current device and its stream's handle, without building a torch.cuda.Stream (3 us a call); by the public functions
-# where torch has no such names (a build without CUDA, which can still load the library and make its refusals).
+# The current device and its stream's handle, without building a torch.cuda.Stream (3 us a call); by the public
+# functions where torch has no such names (a build without CUDA, which can still load the library and make its refusals).
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda device: torch.cuda.current_stream(device).cuda_stream)

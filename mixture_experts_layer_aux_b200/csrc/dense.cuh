@@ -28,6 +28,11 @@
 // workspace (at most two per CTA; a piece that holds a whole tile finishes it),
 // and fixup_kernel adds them in the order of K and applies the epilogue, so
 // results do not depend on timing.
+//
+// Times in the comments below compare variants within one run. The large cases
+// are slower in long runs, under the power cap (8192 tokens in MXFP8, H = 7168,
+// F = 2048: 265 us in runs of 2 ms, 308 in one of seconds; a training step of
+// 4096 tokens, H = 4096, F = 14336: 2930 and 3400).
 #pragma once
 
 #include <algorithm>
@@ -249,8 +254,8 @@ MOE_DEV void commit(uint64_t* bar) {
                    : "memory");
   }
 }
-// Arrives on the first CTA's barrier, relaxed. For accumulators that is all: they are in registers (tcgen05.wait::ld and
-// the tcgen05 fences order them). Scales are ordinary stores to this SM's shared memory which the first CTA's
+// Arrives on the first CTA's barrier, relaxed. For accumulators that is all: they are in registers (tcgen05.wait::ld
+// and the tcgen05 fences order them). Scales are ordinary stores to this SM's shared memory which the first CTA's
 // tcgen05.cp reads, and a proxy fence orders no threads: release_smem_cluster() goes before their arrival, and the
 // issuer waits with the matching acquire. A release of all memory at the cluster's scope would also wait for every
 // access to global memory in flight: 1 us per tile, and 0.9 us per k-block of MXFP8, whose MMAs take 0.35.
@@ -584,9 +589,9 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
     // needs all). They join their stage: the loader waits for the stage as the producer does, and arrives on its
     // barrier. A lane reads the words of SF_KB k-blocks of rows l, l + 32, l + 64, l + 96 of a block of 128, one batch
     // ahead, and writes, per k-block, these rows' words as the 16 bytes l of its chunk; one proxy fence for two
-    // k-blocks, and no more instructions than that takes: they set the pace (8192 tokens, H = 7168, F = 2048: 270 us;
-    // with the rows' addresses computed for each batch 290, with a second loader and a fence for each k-block besides
-    // 298, with barriers of their own for four k-blocks at a time 360).
+    // k-blocks, and no more instructions than that takes: they set the pace (8192 tokens, H = 7168, F = 2048, in short
+    // runs: 270 us when it was made; with the rows' addresses computed for each batch 290, with a second loader and a
+    // fence for each k-block besides 298, with barriers of their own for four k-blocks at a time 360).
     if constexpr (C::MX) {
       uint32_t cur[C::SF_BLOCKS][4][SF_KB], nxt[C::SF_BLOCKS][4][SF_KB];
       Seg s = walk.next(p);
@@ -837,7 +842,8 @@ __global__ void __launch_bounds__(Cfg<OP, CG, BN>::THREADS, 1) gemm_kernel(const
 
 // Adds the partial accumulators of every tile that was cut (at most MAX_PIECES) and applies the epilogue. Item: one
 // row and 8 output columns; grid.x: tiles. With many pieces, SPLIT = 4 threads take every fourth, and are added in
-// a fixed order (8 tiles in 18 pieces each: 17 us by one thread; 64 tiles in 2 or 3: 14 by four, 10.7 by one).
+// a fixed order (the block's forward, T = 115, H = 2432, F = 12440, 10 tiles in 7 pieces each: 53.2 us by four, 55.6 by
+// one; T = 333, H = 2056, F = 5464, 34 tiles in 2: 47.0 by four, 45.1 by one).
 constexpr int FIX_THREADS = 256;
 constexpr int MAX_PIECES = 16, MANY_PIECES = 6;
 template <int OP, int CG, int BN, int SPLIT>

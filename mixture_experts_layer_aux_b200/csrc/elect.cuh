@@ -22,9 +22,9 @@ MOE_DEV bool elect_one() {
 MOE_DEV bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int code) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, code));
 }
-// The same for a barrier on which another CTA of the cluster arrives with relaxed.cluster after release_smem_cluster():
-// that CTA's ordinary stores to its shared memory are visible after it. The phase is observed at the cluster's scope, and
-// the acquire is restricted to shared memory, so that it waits for no access to global memory.
+// The same for a barrier on which another CTA of the cluster arrives with relaxed.cluster after
+// release_smem_cluster(): that CTA's ordinary stores to its shared memory are visible after it. The phase is observed at
+// the cluster's scope, and the acquire is restricted to shared memory, so that it waits for no access to global memory.
 MOE_DEV bool mbar_wait_warp_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int code) {
   uint32_t ok = 0;
   uint64_t t0 = 0;

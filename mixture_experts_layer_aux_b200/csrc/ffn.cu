@@ -16,10 +16,24 @@ namespace ffn {
 
 using dense::Params;
 
-// Tokens up to which the streaming kernels are taken: 56 (bf16, H = 2048, F = 5504: 48 tokens 28.7 us streaming and
-// 30.9 dense, 64 tokens 32.6 and 30.6; 4096 x 14336: 72.9 and 75.3, 74.9 and 76.1), 16 for MXFP8, whose loader of scales
-// sets the pace there (H = 7168, F = 2048: 16 tokens 23.4 us and, at an earlier stage of both, 26.9 and 30.6; 32 tokens
-// then 31.0 and 28.0, now dense 27.2).
+// Tokens up to which the streaming kernels are taken, whatever the widths: 56 in bf16, 16 in MXFP8. Streaming / dense,
+// us:
+//   bf16, H x F      48 tokens      56             64
+//   8192 x 28672     243  / 264     244  / 258     250  / 251
+//   4096 x 14336     75.4 / 75.5    74.6 / 76.3    78.4 / 77.2
+//   4096 x 11008     61.9 / 64.7    62.7 / 63.1    64.0 / 65.1
+//   2048 x 5504      28.6 / 30.7    30.8 / 30.8    32.6 / 30.6
+//   2056 x 5464      32.8 / 31.0    35.6 / 31.9    36.9 / 31.0
+//   1024 x 4096      22.5 / 22.5    24.1 / 22.5    24.6 / 20.8
+//   MXFP8            16             24             32
+//   7168 x 18432     90.7 / 95.3    92.1 / 92.3    92.0 / 88.4
+//   4096 x 14336     45.5 / 51.9    49.0 / 52.4    49.2 / 49.2
+//   7168 x 2048      22.8 / 30.7    25.9 / 28.2    28.5 / 26.7
+//   4096 x 4096      22.5 / 30.4    24.6 / 30.6    27.0 / 28.4
+//   1024 x 4096      17.7 / 20.5    20.4 / 20.5    22.3 / 20.6
+// So ragged and small widths lose up to 4 us below 57 tokens. In MXFP8, room for 32 tokens in the loader of scales
+// (which the figures from 24 on have) costs the calls of fewer 0 to 2 us each: 16 tokens 7168 x 2048 24.5, 8 tokens
+// 4096 x 4096 22.4 in place of 20.6.
 static bool streams(const moe_ffn_config* c) {
   return c->T <= (c->dtype == MOE_DT_MXFP8 ? stream::MAX_T_MX : stream::MAX_T);
 }

@@ -8,6 +8,11 @@
 //
 // Both are bound by memory: a row is read once, held in registers (V vectors
 // of 8 bf16 per thread), reduced with one block barrier and written once.
+// Of the backward this holds up to H = 8192 (8192 rows with dh: H = 4096 49 us,
+// 7168 85, 8192 94, 0.83 to 0.88 of the copy's rate). With V = 4 the row, the next
+// one and the weight gradient are more than the registers hold: 200 bytes a
+// thread, 400 with dh, go through local memory, and one CTA fits an SM
+// (H = 12288 301 us, 16384 358, 0.41 and 0.46).
 // CTAs are persistent over rows, so the weight stays in registers and the next
 // row's loads are in flight while the current row is reduced and written. Rows
 // are counted unsigned: T goes up to 2^31 - 1, and a CTA's next row passes it.

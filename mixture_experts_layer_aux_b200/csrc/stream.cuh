@@ -69,7 +69,7 @@ constexpr int MAX_N = 224;                // s T at most (two accumulators and t
 // SF_SLOTS - SF_AHEAD stages.
 constexpr int SF_SLOTS = 8, SF_AHEAD = 2;
 constexpr int SF_SLOT_COLS = 12;          // scale columns of a stage in TMEM (W0, W1, x: 128 rows each)
-constexpr int MAX_PARTS = 9;              // K blocks of a stage, at most 8 (4 with MXFP8), and the tail
+constexpr int MAX_BLOCKS = 8, MAX_BLOCKS_MX = 4;  // K blocks of a stage
 constexpr int MAX_CLUSTER = 4;            // CTAs that share a tile, each taking a part of K
 constexpr int BAR_BYTES = 1024;
 // Bytes of the ring. A CTA with little to stream (up to SHORT_BYTES in all) leaves room for one of the other kernel
@@ -786,7 +786,7 @@ Params plan(int T, int N, int K) {
   // operand rows, TMEM and the ring allow
   float best = 1e30f;
   for (int merged = 0; merged <= (GATEUP && one ? 1 : 0); ++merged)
-    for (int s = 1; s <= (one && p.z ? (MX ? 4 : MAX_PARTS - 1) : 1); s += MX ? s : 1) {
+    for (int s = 1; s <= (one && p.z ? (MX ? MAX_BLOCKS_MX : MAX_BLOCKS) : 1); s += MX ? s : 1) {
       const int rows = (s * p.r + 7) / 8 * 8, n = (s * T + 15) / 16 * 16, ops = GATEUP && !merged ? 2 : 1;
       if (rows * (merged ? 2 : 1) > 128 || (s > 1 && (s * T > MAX_N || s > p.KB))) continue;
       const int stage = (GATEUP ? 2 : 1) * rows * ROW_BYTES + n * ROW_BYTES;
